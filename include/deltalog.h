@@ -220,6 +220,133 @@ int dl_state_fill(const dl_state* st, int32_t* fill_out);
 /* Releases the handle (not the borrowed buffers).  NULL is accepted. */
 int dl_state_destroy(dl_state* st);
 
+/* ------------------------------------------------------------------------
+ * Operators around the recurrent step: the short causal convolution that
+ * feeds q, k and v, the selective state space recurrence (whose state has the
+ * layout of every other recurrence here), and the residual RMS norm that turns
+ * a layer's rows into the next projection's input.  They keep no state of
+ * their own: every buffer is the caller's, and the conventions above hold
+ * (checks on the host first, asynchronous on `stream`, no device memory
+ * allocated, tensors on the current device).  The prompt forms take packed
+ * sequences: starts is a host array of n + 1 non-decreasing int32 >= 0, and
+ * sequence s holds the rows starts[s] .. starts[s+1] - 1 (it may be empty);
+ * rows outside [starts[0], starts[n]) are neither read nor written.  Lengths
+ * travel by value with the launch, so a captured CUDA graph replays the
+ * captured lengths; the single-token forms and dl_norm depend on nothing but
+ * their buffers.  Row strides (ld*) count elements and may exceed the row, so
+ * a row may be a range of columns of a wider one; an output must not share
+ * elements with an input unless its comment says so.  Each call's result does
+ * not depend on how the work is split, but for the rounding of sums. */
+
+/* Element type of dl_norm's output, beside DL_F32 and DL_BF16. */
+enum dl_out_dtype { DL_E4M3 = 2 /* 8 bits: 4 exponent, 3 mantissa, largest value 448 (e4m3) */ };
+
+/* dl_conv_config.flags */
+enum dl_conv_flags { DL_CONV_SILU = 1 /* y * sigmoid(y) on the way out */ };
+
+/* Depthwise causal convolution of width W in {2, 3, 4} over C channels. */
+typedef struct dl_conv_config {
+  int32_t C;        /* channels, >= 1 */
+  int32_t W;        /* taps */
+  int32_t in_dtype; /* enum dl_dtype of x, y and the states */
+  int32_t flags;    /* enum dl_conv_flags */
+} dl_conv_config;
+
+/* y[t, c] = act(bias[c] + sum_j w[c, j] x[t - W + 1 + j, c]) for packed
+ * sequences; rows before a sequence's first token come from its state.
+ *   x, y: in_dtype rows of C (strides ldx, ldy >= C); y must not be x
+ *   w: fp32 [C, W] (the last tap meets the current token); bias: fp32 [C] or NULL
+ *   h0: in_dtype [n, W-1, C], each sequence's last W - 1 input rows, oldest
+ *       first, or NULL for zeros;  h1: the same after the call, or NULL;
+ *       h1 may be h0.  An empty sequence passes its state on.
+ * Pointers need their element's alignment only; 16-byte aligned pointers and
+ * strides, and C a multiple of 16 bytes, take the wide path.
+ * Errors: DL_ERR_ARG, DL_ERR_ALIGN, DL_ERR_UNSUPPORTED (W). */
+int dl_conv_prompt(const dl_conv_config* cfg, int32_t n, const int32_t* starts, const void* x,
+                   int64_t ldx, const float* w, const float* bias, const void* h0, void* h1,
+                   void* y, int64_t ldy, void* stream);
+
+/* The same for one token of each of B sequences: row b of x and y, and the
+ * state h [B, W-1, C], which is updated in place. */
+int dl_conv_step(const dl_conv_config* cfg, int32_t B, const void* x, int64_t ldx, const float* w,
+                 const float* bias, void* h, void* y, int64_t ldy, void* stream);
+
+/* dl_ssm_config.flags */
+enum dl_ssm_flags { DL_SSM_SOFTPLUS = 1 /* dt = softplus(dt_raw + dt_bias) */ };
+
+/* Selective state space recurrence with a scalar decay per head and token:
+ *   dt = dt_raw + dt_bias (through softplus with DL_SSM_SOFTPLUS), dt >= 0
+ *   S_t = e^{dt a_h} S_{t-1} + dt v_t k_t^T,   o_t = S_t q_t + d_h v_t
+ * with S fp32 [d_v, d_k] per head, and q, k shared by the H / G heads of a
+ * group (head h reads group h / (H / G)).  d_k, d_v in {64, 128}. */
+typedef struct dl_ssm_config {
+  int32_t H;        /* heads */
+  int32_t G;        /* groups of q and k; divides H */
+  int32_t d_k;
+  int32_t d_v;
+  int32_t in_dtype; /* enum dl_dtype of q, k, v and o */
+  int32_t flags;    /* enum dl_ssm_flags */
+} dl_ssm_config;
+
+/* Rows of one call.  q, k, v and o: 16-byte aligned, strides multiples of 16
+ * bytes.  a <= 0 and dt >= 0 keep every factor in (0, 1].  A value that is
+ * not finite makes the outputs of its own sequence (and head, or group)
+ * undefined from its 128-token tile on, and no others. */
+typedef struct dl_ssm_io {
+  const void* q;        /* [T, G, d_k] */
+  const void* k;        /* [T, G, d_k] */
+  const void* v;        /* [T, H, d_v] */
+  const float* dt;      /* [T, H] dt_raw */
+  const float* a;       /* [H] */
+  const float* d;       /* [H] or NULL (zeros) */
+  const float* dt_bias; /* [H] or NULL (zeros) */
+  void* o;              /* [T, H, d_v] */
+  int64_t ldq, ldk, ldv, lddt, ldo; /* row strides in elements */
+} dl_ssm_io;
+
+/* Bytes of device workspace dl_ssm_prompt needs for these lengths on the
+ * current device (may be 0). */
+int dl_ssm_bytes(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, size_t* bytes);
+
+/* Packed prompts.  S0: fp32 [n, H, d_v, d_k] states before the first token,
+ * or NULL for zeros; S1: the states after the last, or NULL; S1 may be S0 (a
+ * prompt taken in pieces).  The state of a sequence can be loaded by
+ * dl_state_load_seqs or stepped by dl_ssm_step.  workspace: 256-byte aligned,
+ * of workspace_bytes >= dl_ssm_bytes (NULL when that is 0), written by the
+ * call: calls that may run at the same time need one each. */
+int dl_ssm_prompt(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, const dl_ssm_io* io,
+                  const float* S0, float* S1, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* One token of each of B sequences: row b of the io buffers and the state
+ * S [B, H, d_v, d_k] (16-byte aligned), updated in place. */
+int dl_ssm_step(const dl_ssm_config* cfg, int32_t B, const dl_ssm_io* io, float* S, void* stream);
+
+/* Root-mean-square norm of rows, after the addition of a residual:
+ *   h = x + res,  n = h / sqrt(mean(h^2) + eps) * w,  all in fp32.
+ * out_dtype DL_F32 / DL_BF16: out = n, rounded once.  DL_E4M3: per block of
+ * `block` channels (0: the whole row) scale = amax / 448 and code =
+ * e4m3(n * (448 / amax)), round to nearest even; a block with amax < 2^-120
+ * stores zero codes and scale 0. */
+typedef struct dl_norm_config {
+  int32_t D;         /* row length, 1 .. 16384 */
+  int32_t in_dtype;  /* enum dl_dtype of x, res and res_out */
+  int32_t out_dtype; /* enum dl_dtype or DL_E4M3 */
+  int32_t block;     /* DL_E4M3: 128 or 0; else 0 */
+  float eps;         /* >= 0 */
+} dl_norm_config;
+
+/*   x, res, res_out: in_dtype rows of D (strides ldx, ldr, ldro); res may be
+ *   NULL (h = x); res_out takes h rounded to in_dtype, may be NULL, and may be
+ *   x or res (the residual stream updated in place).
+ *   w: fp32 [D];  out: rows of D of out_dtype (stride ldo)
+ *   scales: fp32 [rows, ceil(D / 128)], or [rows] with block 0; NULL unless DL_E4M3.
+ * Pointers need their element's alignment only, as for dl_conv_prompt.
+ * Errors: DL_ERR_ARG, DL_ERR_ALIGN, DL_ERR_UNSUPPORTED (D). */
+int dl_norm(const dl_norm_config* cfg, int64_t rows, const void* x, int64_t ldx, const void* res,
+            int64_t ldr, const float* w, void* res_out, int64_t ldro, void* out, int64_t ldo,
+            float* scales, void* stream);
+
 /* Reads and optionally clears the device error word that kernels set when
  * a bounded wait gives up or a device-side check fails (code 0 = none;
  * *head = first failing head).  Synchronizes `stream`.
@@ -227,11 +354,10 @@ int dl_state_destroy(dl_state* st);
  *     step or a merge means some head's work was skipped part-way (a step
  *     may already have advanced that head's fill, a merge may have folded
  *     only some rows): the state is invalid until dl_state_reset.
- *   - `st` NULL reads the one word per device that every dl_eager_step call
- *     and dl_selftest_wait_timeout share: the first error recorded wins, so
- *     with overlapping eager calls the head index may belong to either, and
- *     the self-test clears the word (erasing what an earlier eager call
- *     recorded). */
+ *   - `st` NULL reads the one word per device that every dl_eager_step call,
+ *     dl_ssm_prompt call and dl_selftest_wait_timeout share: the first error recorded wins, so
+ *     with overlapping calls the head index may belong to either, and the
+ *     self-test clears the word (erasing what an earlier call recorded). */
 int dl_device_error(dl_state* st, int32_t* code, int32_t* head, int clear, void* stream);
 
 /* Exercises the kernels' failure path on the current device without a

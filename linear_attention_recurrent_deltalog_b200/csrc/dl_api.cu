@@ -14,6 +14,7 @@
 
 #include "deltalog.h"
 #include "dl_launch.cuh"
+#include "dl_layer.cuh"
 
 namespace {
 
@@ -284,6 +285,11 @@ __global__ void dl_selftest_wait_kernel(int* err) {
 }
 
 }  // namespace
+
+namespace dl {
+void count_launches(int n) { g_launches.fetch_add(uint64_t(n), std::memory_order_relaxed); }
+int* shared_err_word() { return global_err_word(); }
+}  // namespace dl
 
 struct dl_state {
   dl_config cfg;

@@ -17,9 +17,11 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional, Sequence
 
+import numpy as np
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdeltalog.so")
@@ -34,10 +36,14 @@ DL_MERGE_FULL, DL_MERGE_ALL = 0, 1
 DL_FLAG_FUSED_MERGE = 1
 DL_FLAG_KLA = 4
 DL_FLAG_BASE_Q8 = 8
+DL_E4M3 = 2
+DL_CONV_SILU = 1
+DL_SSM_SOFTPLUS = 1
 
 VARIANT_IDS = {"gdn": DL_GDN, "kda": DL_KDA, "rwkv6": DL_RWKV6, "gdn2": DL_GDN2}
 DTYPE_IDS = {"f32": DL_F32, "bf16": DL_BF16}
-_TORCH_IN = {DL_F32: torch.float32, DL_BF16: torch.bfloat16}
+OUT_DTYPE_IDS = {**DTYPE_IDS, "e4m3": DL_E4M3}
+_TORCH_IN = {DL_F32: torch.float32, DL_BF16: torch.bfloat16, DL_E4M3: torch.float8_e4m3fn}
 
 
 def _load() -> ctypes.CDLL:
@@ -57,10 +63,33 @@ class dl_config(ctypes.Structure):
         [("kla_eps", ctypes.c_float)]
 
 
+class dl_conv_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("C", "W", "in_dtype", "flags")]
+
+
+class dl_ssm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("H", "G", "d_k", "d_v", "in_dtype", "flags")]
+
+
+class dl_ssm_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "dt", "a", "d", "dt_bias", "o")] + \
+        [(n, ctypes.c_int64) for n in ("ldq", "ldk", "ldv", "lddt", "ldo")]
+
+
+class dl_norm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("D", "in_dtype", "out_dtype", "block")] + \
+        [("eps", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SZ = ctypes.POINTER(ctypes.c_size_t)
 _CFG = ctypes.POINTER(dl_config)
+_CONV = ctypes.POINTER(dl_conv_config)
+_SSM = ctypes.POINTER(dl_ssm_config)
+_SSM_IO = ctypes.POINTER(dl_ssm_io)
+_NORM = ctypes.POINTER(dl_norm_config)
 
 _SIGS = {
     "dl_state_bytes": (_I, [_CFG, _SZ, _SZ, _SZ]),
@@ -71,6 +100,12 @@ _SIGS = {
     "dl_merge": (_I, [_P, _I, _P]),
     "dl_materialize": (_I, [_P, _P, _P]),
     "dl_eager_step": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "dl_conv_prompt": (_I, [_CONV, _I, _P, _P, _L, _P, _P, _P, _P, _P, _L, _P]),
+    "dl_conv_step": (_I, [_CONV, _I, _P, _L, _P, _P, _P, _P, _L, _P]),
+    "dl_ssm_bytes": (_I, [_SSM, _I, _P, _SZ]),
+    "dl_ssm_prompt": (_I, [_SSM, _I, _P, _SSM_IO, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dl_ssm_step": (_I, [_SSM, _I, _SSM_IO, _P, _P]),
+    "dl_norm": (_I, [_NORM, _L, _P, _L, _P, _L, _P, _P, _L, _P, _L, _P, _P]),
     "dl_state_fill": (_I, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "dl_state_destroy": (_I, [_P]),
     "dl_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32),
@@ -153,6 +188,78 @@ class Config:
         return _TORCH_IN[DTYPE_IDS[self.in_dtype]]
 
 
+@dataclasses.dataclass(frozen=True)
+class ConvConfig:
+    """Python mirror of ``dl_conv_config``: a depthwise causal convolution of
+    ``W`` taps over ``C`` channels."""
+
+    C: int
+    W: int
+    in_dtype: str = "bf16"
+    silu: bool = True
+
+    @functools.cached_property
+    def c(self) -> dl_conv_config:
+        return dl_conv_config(self.C, self.W, DTYPE_IDS[self.in_dtype],
+                              DL_CONV_SILU if self.silu else 0)
+
+    @functools.cached_property
+    def torch_in_dtype(self) -> torch.dtype:
+        return _TORCH_IN[DTYPE_IDS[self.in_dtype]]
+
+
+@dataclasses.dataclass(frozen=True)
+class SsmConfig:
+    """Python mirror of ``dl_ssm_config``: ``H`` heads of d_v x d_k states, q
+    and k shared by the heads of each of ``G`` groups."""
+
+    H: int
+    G: int
+    d_k: int
+    d_v: int
+    in_dtype: str = "bf16"
+    softplus: bool = True
+
+    @functools.cached_property
+    def c(self) -> dl_ssm_config:
+        return dl_ssm_config(self.H, self.G, self.d_k, self.d_v, DTYPE_IDS[self.in_dtype],
+                             DL_SSM_SOFTPLUS if self.softplus else 0)
+
+    @functools.cached_property
+    def torch_in_dtype(self) -> torch.dtype:
+        return _TORCH_IN[DTYPE_IDS[self.in_dtype]]
+
+
+@dataclasses.dataclass(frozen=True)
+class NormConfig:
+    """Python mirror of ``dl_norm_config``: rows of ``D``; ``out_dtype`` "f32",
+    "bf16" or "e4m3", the last with one scale per ``block`` (128) channels or
+    per row (0)."""
+
+    D: int
+    in_dtype: str = "bf16"
+    out_dtype: str = "bf16"
+    block: int = 0
+    eps: float = 1e-6
+
+    @functools.cached_property
+    def c(self) -> dl_norm_config:
+        return dl_norm_config(self.D, DTYPE_IDS[self.in_dtype], OUT_DTYPE_IDS[self.out_dtype],
+                              self.block, float(self.eps))
+
+    @functools.cached_property
+    def torch_in_dtype(self) -> torch.dtype:
+        return _TORCH_IN[DTYPE_IDS[self.in_dtype]]
+
+    @functools.cached_property
+    def torch_out_dtype(self) -> torch.dtype:
+        return _TORCH_IN[OUT_DTYPE_IDS[self.out_dtype]]
+
+    @property
+    def scales_per_row(self) -> int:
+        return -(-self.D // self.block) if self.block else 1
+
+
 # ----------------------------------------------------------------- marshalling
 
 def _ptr(x) -> Optional[int]:
@@ -202,6 +309,56 @@ def _check_step_tensors(cfg: Config, q, k, v, decay, beta, bonus, o) -> None:
     else:
         _need(beta, "beta", BH, torch.float32)
     _need(o, "o", BH * dv, torch.float32)
+
+
+def _rows(t, name: str, rows: int, cols: int, dtype: torch.dtype) -> int:
+    """Checks a tensor of at least ``rows`` rows of ``cols`` elements and
+    returns its row stride: [rows, cols], or [rows, a, b] with a * b = cols,
+    whose rows may lie apart but are contiguous themselves."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    shape = t.shape
+    if len(shape) == 2:
+        ok = shape[1] == cols and (cols == 1 or t.stride(1) == 1)
+    else:
+        ok = len(shape) == 3 and shape[1] * shape[2] == cols and \
+            (shape[0] == 0 or t[0].is_contiguous())
+    if not ok:
+        raise ValueError(f"{name}: expected rows of {cols} contiguous elements, got shape "
+                         f"{tuple(shape)} with strides {t.stride()}")
+    if shape[0] < rows:
+        raise ValueError(f"{name}: {shape[0]} rows, need {rows}")
+    if shape[0] <= 1:
+        return cols  # the one row's stride is never used
+    ld = t.stride(0)
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld}, {cols} elements)")
+    return ld
+
+
+def _on_device(tensors) -> None:
+    """Every tensor on the current CUDA device (whose stream the call uses)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors:
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if t is not None and (dev is None or t.get_device() != dev):
+            raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+
+
+def _starts(starts):
+    """-> (host int32 array, n, rows): sequence s holds rows starts[s] .. starts[s+1] - 1."""
+    a = starts if isinstance(starts, np.ndarray) else np.asarray(starts)
+    if a.ndim != 1 or a.size < 1 or a.dtype.kind not in "iu":
+        raise ValueError("starts: expected n + 1 integers on the host")
+    if a.dtype != np.int32:
+        if a.size and (int(a.min()) < 0 or int(a.max()) > 0x7fffffff):
+            raise ValueError("starts: must fit int32 and be >= 0")
+        a = a.astype(np.int32)
+    a = np.ascontiguousarray(a)
+    return a, a.size - 1, int(a[-1])
 
 
 # ----------------------------------------------------------------- C entry points
@@ -266,6 +423,115 @@ def dl_eager_step(cfg: Config, S, q, k, v, decay, beta, bonus, o, stream=None) -
     c = cfg.c()
     _check(_lib.dl_eager_step(ctypes.byref(c), _ptr(S), _ptr(q), _ptr(k), _ptr(v), _ptr(decay),
                               _ptr(beta), _ptr(bonus), _ptr(o), _stream(stream)), "dl_eager_step")
+
+
+def _conv_args(cfg: ConvConfig, rows: int, n: int, x, w, bias, h0, h1, y):
+    t = cfg.torch_in_dtype
+    ldx = _rows(x, "x", rows, cfg.C, t)
+    ldy = _rows(y, "y", rows, cfg.C, t)
+    _need(w, "w", cfg.C * cfg.W, torch.float32)
+    _need(bias, "bias", cfg.C, torch.float32)
+    _need(h0, "h0", n * (cfg.W - 1) * cfg.C, t)
+    _need(h1, "h1", n * (cfg.W - 1) * cfg.C, t)
+    _on_device((("x", x), ("w", w), ("bias", bias), ("h0", h0), ("h1", h1), ("y", y)))
+    return ldx, ldy
+
+
+def dl_conv_prompt(cfg: ConvConfig, starts, x, w, bias, h0, h1, y, stream=None) -> None:
+    """y = short causal convolution of packed sequences; ``h0`` (or None) and
+    ``h1`` (or None, or ``h0``) are the states [n, W-1, C] before and after."""
+    a, n, rows = _starts(starts)
+    ldx, ldy = _conv_args(cfg, rows, n, x, w, bias, h0, h1, y)
+    _check(_lib.dl_conv_prompt(ctypes.byref(cfg.c), n, a.ctypes.data, x.data_ptr(), ldx,
+                               w.data_ptr(), _ptr(bias), _ptr(h0), _ptr(h1), y.data_ptr(), ldy,
+                               _stream(stream)), "dl_conv_prompt")
+
+
+def dl_conv_step(cfg: ConvConfig, x, w, bias, h, y, stream=None) -> None:
+    """One token of each of x.shape[0] sequences; the state ``h`` is updated in place."""
+    B = x.shape[0]
+    ldx, ldy = _conv_args(cfg, B, B, x, w, bias, h, None, y)
+    if h is None:
+        raise TypeError("h: expected a torch.Tensor")
+    _check(_lib.dl_conv_step(ctypes.byref(cfg.c), B, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias),
+                             h.data_ptr(), y.data_ptr(), ldy, _stream(stream)), "dl_conv_step")
+
+
+def dl_ssm_bytes(cfg: SsmConfig, starts) -> int:
+    """Bytes of workspace ``dl_ssm_prompt`` needs for these lengths."""
+    a, n, _ = _starts(starts)
+    b = ctypes.c_size_t()
+    _check(_lib.dl_ssm_bytes(ctypes.byref(cfg.c), n, a.ctypes.data, ctypes.byref(b)),
+           "dl_ssm_bytes")
+    return b.value
+
+
+def _ssm_io(cfg: SsmConfig, rows: int, n: int, q, k, v, dt, a, d, dt_bias, o, S0, S1):
+    t, H = cfg.torch_in_dtype, cfg.H
+    nk, nv = cfg.G * cfg.d_k, H * cfg.d_v
+    ld = (_rows(q, "q", rows, nk, t), _rows(k, "k", rows, nk, t), _rows(v, "v", rows, nv, t),
+          _rows(dt, "dt", rows, H, torch.float32), _rows(o, "o", rows, nv, t))
+    if a is None:
+        raise TypeError("a: expected a torch.Tensor")
+    for name, x in (("a", a), ("d", d), ("dt_bias", dt_bias)):
+        _need(x, name, H, torch.float32)
+    _need(S0, "S0", n * nv * cfg.d_k, torch.float32)
+    _need(S1, "S1", n * nv * cfg.d_k, torch.float32)
+    _on_device((("q", q), ("k", k), ("v", v), ("dt", dt), ("a", a), ("d", d),
+                ("dt_bias", dt_bias), ("o", o), ("S0", S0), ("S1", S1)))
+    return dl_ssm_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), a.data_ptr(),
+                     _ptr(d), _ptr(dt_bias), o.data_ptr(), *ld)
+
+
+def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o, workspace=None,
+                  stream=None) -> None:
+    """Selective state space scan of packed sequences; ``S0`` (or None) and
+    ``S1`` (or None, or ``S0``) are the states [n, H, d_v, d_k] before and
+    after.  ``workspace``: a uint8 tensor of ``dl_ssm_bytes`` (allocated for
+    the call when None)."""
+    arr, n, rows = _starts(starts)
+    io = _ssm_io(cfg, rows, n, q, k, v, dt, a, d, dt_bias, o, S0, S1)
+    if workspace is None:
+        workspace = torch.empty(dl_ssm_bytes(cfg, arr), dtype=torch.uint8, device=q.device)
+    nb = workspace.numel() * workspace.element_size()
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    _on_device((("workspace", workspace),))
+    _check(_lib.dl_ssm_prompt(ctypes.byref(cfg.c), n, arr.ctypes.data, ctypes.byref(io), _ptr(S0),
+                              _ptr(S1), workspace.data_ptr() if nb else None, nb,
+                              _stream(stream)), "dl_ssm_prompt")
+
+
+def dl_ssm_step(cfg: SsmConfig, q, k, v, dt, a, d, dt_bias, S, o, stream=None) -> None:
+    """One token of each of q.shape[0] sequences; the state ``S`` [B, H, d_v,
+    d_k] is updated in place."""
+    B = q.shape[0]
+    io = _ssm_io(cfg, B, B, q, k, v, dt, a, d, dt_bias, o, S, None)
+    if S is None:
+        raise TypeError("S: expected a torch.Tensor")
+    _check(_lib.dl_ssm_step(ctypes.byref(cfg.c), B, ctypes.byref(io), S.data_ptr(),
+                            _stream(stream)), "dl_ssm_step")
+
+
+def dl_norm(cfg: NormConfig, x, w, out, res=None, res_out=None, scales=None, stream=None) -> None:
+    """out = RMS norm of x (+ res), times w; ``res_out`` takes x + res.  An
+    "e4m3" output needs ``scales`` [rows, cfg.scales_per_row]."""
+    rows, t = x.shape[0], cfg.torch_in_dtype
+    ldx = _rows(x, "x", rows, cfg.D, t)
+    ldo = _rows(out, "out", rows, cfg.D, cfg.torch_out_dtype)
+    ldr = _rows(res, "res", rows, cfg.D, t) if res is not None else cfg.D
+    ldro = _rows(res_out, "res_out", rows, cfg.D, t) if res_out is not None else cfg.D
+    if w is None:
+        raise TypeError("w: expected a torch.Tensor")
+    _need(w, "w", cfg.D, torch.float32)
+    if cfg.out_dtype == "e4m3" and scales is None:
+        raise TypeError("scales: expected a torch.Tensor for an e4m3 output")
+    _need(scales, "scales", rows * cfg.scales_per_row, torch.float32)
+    _on_device((("x", x), ("w", w), ("out", out), ("res", res), ("res_out", res_out),
+                ("scales", scales)))
+    _check(_lib.dl_norm(ctypes.byref(cfg.c), rows, x.data_ptr(), ldx, _ptr(res), ldr, w.data_ptr(),
+                        _ptr(res_out), ldro, out.data_ptr(), ldo, _ptr(scales), _stream(stream)),
+           "dl_norm")
 
 
 def dl_state_fill(handle: int, cfg: Config):
