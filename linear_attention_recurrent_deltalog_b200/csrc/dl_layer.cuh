@@ -55,6 +55,15 @@ cudaError_t launch_ssm_step(const SsmParams& p, int B, int dk, int dv, bool bf16
 cudaError_t launch_ssm_scan(const SsmParams& p, int n, const int32_t* starts, int dk, int dv,
                             bool bf16, cudaStream_t s);
 
+// How a prompt call is cut along its sequences, and the workspace that takes.
+struct SsmPlan {
+  int tile_tokens;
+  size_t bytes;
+};
+SsmPlan plan_ssm(int H, int G, int dk, int dv, int n, const int32_t* starts, int sms);
+cudaError_t launch_ssm_chunked(const SsmParams& p, int n, const int32_t* starts, int dk, int dv,
+                               const SsmPlan& plan, void* ws, cudaStream_t s);
+
 constexpr int kOutF32 = 0, kOutBF16 = 1, kOutE4M3 = 2;
 
 struct NormParams {

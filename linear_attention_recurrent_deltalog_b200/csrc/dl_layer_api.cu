@@ -109,6 +109,18 @@ dl::SsmParams ssm_params(const dl_ssm_config& c, const dl_ssm_io& io, const floa
   return p;
 }
 
+// SMs the plan of a prompt call reckons with.  Without a device (sizes asked
+// for on the host alone) a B200's.
+int plan_sms() {
+  const int n = dl::sm_count();
+  return n > 0 ? n : 148;
+}
+
+dl::SsmPlan ssm_plan(const dl_ssm_config& c, int32_t n, const int32_t* starts) {
+  if (c.in_dtype != DL_BF16 || n == 0) return dl::SsmPlan{};
+  return dl::plan_ssm(c.H, c.G, c.d_k, c.d_v, n, starts, plan_sms());
+}
+
 int status(cudaError_t e) { return e == cudaSuccess ? DL_OK : DL_ERR_CUDA; }
 
 }  // namespace
@@ -145,7 +157,7 @@ int dl_ssm_bytes(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, siz
   if (bytes == nullptr) return DL_ERR_ARG;
   rc = check_starts(n, starts);
   if (rc != DL_OK) return rc;
-  *bytes = 0;
+  *bytes = ssm_plan(*cfg, n, starts).bytes;
   return DL_OK;
 }
 
@@ -160,14 +172,18 @@ int dl_ssm_prompt(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, co
   if (rc != DL_OK) return rc;
   if (!aligned(S0, 16) || !aligned(S1, 16)) return DL_ERR_ALIGN;
   if (int64_t(n) * cfg->H > 0x7fffffff) return DL_ERR_ARG;
-  size_t need = 0;
-  rc = dl_ssm_bytes(cfg, n, starts, &need);
-  if (rc != DL_OK) return rc;
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return DL_ERR_ARG;
+  const dl::SsmPlan plan = ssm_plan(*cfg, n, starts);
+  if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes)) return DL_ERR_ARG;
   if (!aligned(workspace, 256)) return DL_ERR_ALIGN;
   if (n == 0) return DL_OK;
-  const dl::SsmParams p = ssm_params(*cfg, *io, S0, S1);
-  return status(dl::launch_ssm_scan(p, n, starts, cfg->d_k, cfg->d_v, cfg->in_dtype == DL_BF16,
+  dl::SsmParams p = ssm_params(*cfg, *io, S0, S1);
+  if (cfg->in_dtype == DL_BF16) {
+    p.err = dl::shared_err_word();
+    if (p.err == nullptr) return DL_ERR_CUDA;
+    return status(dl::launch_ssm_chunked(p, n, starts, cfg->d_k, cfg->d_v, plan, workspace,
+                                         static_cast<cudaStream_t>(stream)));
+  }
+  return status(dl::launch_ssm_scan(p, n, starts, cfg->d_k, cfg->d_v, false,
                                     static_cast<cudaStream_t>(stream)));
 }
 
