@@ -259,8 +259,9 @@ typedef struct dl_conv_config {
  *   h0: in_dtype [n, W-1, C], each sequence's last W - 1 input rows, oldest
  *       first, or NULL for zeros;  h1: the same after the call, or NULL;
  *       h1 may be h0.  An empty sequence passes its state on.
- * Pointers need their element's alignment only; 16-byte aligned pointers and
- * strides, and C a multiple of 16 bytes, take the wide path.
+ * Pointers need their element's alignment only; pointers and strides of x, y
+ * and the states in units of four elements, w and bias 16-byte aligned, and C a
+ * multiple of 4 take the wide path.
  * Errors: DL_ERR_ARG, DL_ERR_ALIGN, DL_ERR_UNSUPPORTED (W). */
 int dl_conv_prompt(const dl_conv_config* cfg, int32_t n, const int32_t* starts, const void* x,
                    int64_t ldx, const float* w, const float* bias, const void* h0, void* h1,

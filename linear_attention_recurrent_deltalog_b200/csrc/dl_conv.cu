@@ -2,10 +2,14 @@
 //     y[t, c] = act(bias[c] + sum_j w[c, j] x[t - W + 1 + j, c]),
 // for packed prompts and for single tokens.  Rows before a sequence's first
 // token come from its state (its last W - 1 input rows, oldest first).  Two
-// flops a byte: bound by HBM.  A thread owns VEC neighbouring channels (16
-// bytes) and walks down the tokens of its tile with the last W - 1 rows in
-// registers, so an input row is read once, but for the W - 1 rows at the
-// head of a tile.
+// flops a byte: bound by HBM.  A thread owns VEC neighbouring channels: four
+// where the rows allow 8-byte (bf16) or 16-byte (fp32) accesses, else one.
+// Eight bf16 channels a thread were slower: their taps (fp32, 128 bytes a
+// thread at W = 4) and the rows in flight leave room for a third of the warps.
+// A prompt's thread walks down the tokens of its tile with the last W - 1 rows
+// in registers, so an input row is read once, but for the W - 1 rows at the
+// head of a tile; a step's thread takes several sequences, so that the taps
+// are read once for all of them.
 #include "dl_layer.cuh"
 
 namespace dl {
@@ -14,46 +18,78 @@ namespace {
 
 constexpr int kConvThreads = 256;
 
+// VEC channels of a row as they lie in memory.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1)
-    v[0] = to_f(p[0]);
-  else
-    load_f<VEC>(p, v);
-}
+struct Raw {
+  T e[VEC];
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+  uint2 r;
+};
+template <>
+struct Raw<float, 4> {
+  float4 r;
+};
 
 template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    p[0] = Elem<T>::from_f(v[0]);
-  } else {
-    uint4 r;
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      r = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                     __float_as_uint(v[3]));
-    }
-    *reinterpret_cast<uint4*>(p) = r;
-  }
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
+  return *reinterpret_cast<const Raw<T, VEC>*>(p);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> zero_raw() {
+  Raw<T, VEC> z;
+  memset(&z, 0, sizeof(z));
+  return z;
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 4>& x, float (&v)[4]) {
+  v[0] = __uint_as_float(x.r.x << 16);
+  v[1] = __uint_as_float(x.r.x & 0xffff0000u);
+  v[2] = __uint_as_float(x.r.y << 16);
+  v[3] = __uint_as_float(x.r.y & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack(const Raw<float, 4>& x, float (&v)[4]) {
+  v[0] = x.r.x;
+  v[1] = x.r.y;
+  v[2] = x.r.z;
+  v[3] = x.r.w;
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T, 1>& x, float (&v)[1]) {
+  v[0] = to_f(x.e[0]);
 }
 
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[1]) {
+  p[0] = Elem<T>::from_f(v[0]);
+}
+
+// The taps of channels c .. c + VEC - 1: VEC * W neighbouring floats.
 template <int VEC, int W>
 struct Taps {
-  float w[VEC][W], b[VEC];
+  float w[VEC * W], b[VEC];
   __device__ __forceinline__ Taps(const ConvParams& p, int c) {
+    const float* src = p.w + size_t(c) * W;
+    if constexpr (VEC == 4) {
+      load_f<VEC * W>(src, w);
+      if (p.bias != nullptr) {
+        load_f<VEC>(p.bias + c, b);
+        return;
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[e][j] = p.w[size_t(c + e) * W + j];
-      b[e] = p.bias != nullptr ? p.bias[c + e] : 0.f;
+      for (int j = 0; j < VEC * W; ++j) w[j] = src[j];
     }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) b[e] = p.bias != nullptr ? p.bias[c + e] : 0.f;
   }
 };
 
@@ -69,8 +105,8 @@ __device__ __forceinline__ void taps_row(const Taps<VEC, W>& t, const float (&ol
   for (int e = 0; e < VEC; ++e) {
     float s = t.b[e];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) s = fmaf(t.w[e][j], old[j][e], s);
-    s = fmaf(t.w[e][W - 1], cur[e], s);
+    for (int j = 0; j < W - 1; ++j) s = fmaf(t.w[e * W + j], old[j][e], s);
+    s = fmaf(t.w[e * W + W - 1], cur[e], s);
     y[e] = act ? silu(s) : s;
   }
 }
@@ -87,138 +123,157 @@ __device__ __forceinline__ void shift(float (&old)[W - 1][VEC], const float (&cu
 
 // Row `r` of the state of sequence s (zeros without one).
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void state_row(const ConvParams& p, const void* h, size_t s, int r, int c,
-                                          float (&v)[VEC]) {
-  if (h == nullptr) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = 0.f;
-    return;
-  }
-  load_vec<T, VEC>(static_cast<const T*>(h) + (s * (W - 1) + r) * size_t(p.C) + c, v);
+__device__ __forceinline__ Raw<T, VEC> state_row(const ConvParams& p, size_t s, int r, int c) {
+  if (p.h0 == nullptr) return zero_raw<T, VEC>();
+  return load_raw<T, VEC>(static_cast<const T*>(p.h0) + (s * (W - 1) + r) * size_t(p.C) + c);
 }
 
-template <typename T, int VEC, int W, int TILE, typename Table>
-__global__ void __launch_bounds__(kConvThreads)
-dl_conv_prompt_kernel(const ConvParams p, const __grid_constant__ Table seqs, int seq0, int nvec,
-                      long long total) {
-  const long long id = (long long)blockIdx.x * kConvThreads + threadIdx.x;
+constexpr int kRowsInFlight = 8;
+
+template <typename T, int VEC, int W, typename Table>
+__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 2 ? 3 : 2)
+dl_conv_prompt_kernel(const ConvParams p, const __grid_constant__ Table seqs, int seq0, unsigned nvec,
+                      unsigned total, int tile_rows) {
+  const unsigned id = blockIdx.x * unsigned(kConvThreads) + threadIdx.x;
   if (id >= total) return;
   const int tile = int(id / nvec);
   const int c = int(id % nvec) * VEC;
   const int sl = seqs.find(tile);
   const int begin = seqs.start[sl], end = seqs.start[sl + 1];
   const int first = tile - seqs.tile0[sl];
-  const int t0 = begin + first * TILE;
-  const int t1 = min(t0 + TILE, end);
+  const int t0 = begin + first * tile_rows;
+  const int t1 = min(t0 + tile_rows, end);
   const size_t s = size_t(seq0) + size_t(sl);
   const T* x = static_cast<const T*>(p.x) + c;
   T* y = static_cast<T*>(p.y) + c;
+  constexpr int U = kRowsInFlight;
+  Raw<T, VEC> cur[U];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t + u < t1) cur[u] = load_raw<T, VEC>(x + (long long)(t + u) * p.ldx);
+  };
+  fetch(t0);
   const Taps<VEC, W> taps(p, c);
   float old[W - 1][VEC];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int t = t0 - (W - 1) + j;
-    if (t >= begin)
-      load_vec<T, VEC>(x + (long long)t * p.ldx, old[j]);
-    else
-      state_row<T, VEC, W>(p, p.h0, s, W - 1 + t - begin, c, old[j]);
+    unpack(t >= begin ? load_raw<T, VEC>(x + (long long)t * p.ldx)
+                      : state_row<T, VEC, W>(p, s, W - 1 + t - begin, c),
+           old[j]);
   }
   // The first tile's thread is the only one to read these channels' old
   // state, so it also writes the new one and h1 may be h0.
   if (first == 0 && p.h1 != nullptr) {
-    float nh[W - 1][VEC];
+    Raw<T, VEC> nh[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       const int t = end - (W - 1) + j;
-      if (t >= begin)
-        load_vec<T, VEC>(x + (long long)t * p.ldx, nh[j]);
-      else
-        state_row<T, VEC, W>(p, p.h0, s, W - 1 + t - begin, c, nh[j]);
+      nh[j] = t >= begin ? load_raw<T, VEC>(x + (long long)t * p.ldx)
+                         : state_row<T, VEC, W>(p, s, W - 1 + t - begin, c);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      store_vec<T, VEC>(static_cast<T*>(p.h1) + (s * (W - 1) + j) * size_t(p.C) + c, nh[j]);
+      *reinterpret_cast<Raw<T, VEC>*>(static_cast<T*>(p.h1) + (s * (W - 1) + j) * size_t(p.C) + c) = nh[j];
   }
-  constexpr int U = 8;  // rows in flight
-  int t = t0;
-  for (; t + U <= t1; t += U) {
-    float cur[U][VEC];
-#pragma unroll
-    for (int u = 0; u < U; ++u) load_vec<T, VEC>(x + (long long)(t + u) * p.ldx, cur[u]);
+  for (int t = t0; t < t1; t += U) {
+    if (t != t0) fetch(t);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float o[VEC];
-      taps_row<VEC, W>(taps, old, cur[u], p.silu != 0, o);
-      store_vec<T, VEC>(y + (long long)(t + u) * p.ldy, o);
-      shift<VEC, W>(old, cur[u]);
+      float in[VEC], o[VEC];
+      unpack(cur[u], in);
+      taps_row<VEC, W>(taps, old, in, p.silu != 0, o);
+      if (t + u < t1) store_vec(y + (long long)(t + u) * p.ldy, o);
+      shift<VEC, W>(old, in);
     }
   }
-  for (; t < t1; ++t) {
-    float cur[VEC], o[VEC];
-    load_vec<T, VEC>(x + (long long)t * p.ldx, cur);
-    taps_row<VEC, W>(taps, old, cur, p.silu != 0, o);
-    store_vec<T, VEC>(y + (long long)t * p.ldy, o);
-    shift<VEC, W>(old, cur);
+}
+
+// One token of `rows` sequences (b0, b0 + 1, ..) per thread.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads)
+dl_conv_step_kernel(const ConvParams p, int B, unsigned nvec, unsigned total, int rows) {
+  const unsigned id = blockIdx.x * unsigned(kConvThreads) + threadIdx.x;
+  if (id >= total) return;
+  const int c = int(id % nvec) * VEC;
+  const int b0 = int(id / nvec) * rows, b1 = min(b0 + rows, B);
+  const Taps<VEC, W> taps(p, c);
+  constexpr int U = 4;  // sequences in flight
+  const T* x = static_cast<const T*>(p.x) + c;
+  T* y = static_cast<T*>(p.y) + c;
+  for (int b = b0; b < b1; b += U) {
+    Raw<T, VEC> r[U][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u >= b1) continue;
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) r[u][j] = state_row<T, VEC, W>(p, size_t(b + u), j, c);
+      r[u][W - 1] = load_raw<T, VEC>(x + (long long)(b + u) * p.ldx);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u >= b1) continue;
+      float old[W - 1][VEC], in[VEC], o[VEC];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) unpack(r[u][j], old[j]);
+      unpack(r[u][W - 1], in);
+      taps_row<VEC, W>(taps, old, in, p.silu != 0, o);
+      store_vec(y + (long long)(b + u) * p.ldy, o);
+      T* h = static_cast<T*>(p.h1) + size_t(b + u) * (W - 1) * size_t(p.C) + c;
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+        *reinterpret_cast<Raw<T, VEC>*>(h + size_t(j) * size_t(p.C)) = r[u][j + 1];
+    }
   }
 }
 
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads)
-dl_conv_step_kernel(const ConvParams p, int nvec, long long total) {
-  const long long id = (long long)blockIdx.x * kConvThreads + threadIdx.x;
-  if (id >= total) return;
-  const size_t b = size_t(id / nvec);
-  const int c = int(id % nvec) * VEC;
-  float old[W - 1][VEC], cur[VEC], o[VEC];
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) state_row<T, VEC, W>(p, p.h0, b, j, c, old[j]);
-  load_vec<T, VEC>(static_cast<const T*>(p.x) + (long long)b * p.ldx + c, cur);
-  const Taps<VEC, W> taps(p, c);
-  taps_row<VEC, W>(taps, old, cur, p.silu != 0, o);
-  store_vec<T, VEC>(static_cast<T*>(p.y) + (long long)b * p.ldy + c, o);
-  shift<VEC, W>(old, cur);
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-    store_vec<T, VEC>(static_cast<T*>(p.h1) + (b * (W - 1) + j) * size_t(p.C) + c, old[j]);
-}
+// Threads that fill the device once.
+long long one_wave() { return (long long)(sm_count() > 0 ? sm_count() : 1) * 3 * kConvThreads; }
 
-template <typename T, int VEC, int W, int TILE, int NS>
+template <typename T, int VEC, int W, int NS>
 cudaError_t conv_prompt_range(const ConvParams& p, const int32_t* starts, int s0, int n,
                               cudaStream_t s) {
   SeqTable<NS> tab;
   const int nvec = p.C / VEC;
-  const long long total = fill_seqs(tab, starts, s0, n, TILE) * nvec;
-  const long long grid = (total + kConvThreads - 1) / kConvThreads;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  dl_conv_prompt_kernel<T, VEC, W, TILE, SeqTable<NS>>
-      <<<unsigned(grid), kConvThreads, 0, s>>>(p, tab, s0, nvec, total);
+  // 32 rows a tile re-read 3 of 32; where that leaves the device half empty,
+  // one batch of rows in flight a tile (0.3 us less at T = 300, C = 777)
+  int tile = 4 * kRowsInFlight;
+  long long total = fill_seqs(tab, starts, s0, n, tile) * nvec;
+  if (total < one_wave() / 2) {
+    tile = kRowsInFlight;
+    total = fill_seqs(tab, starts, s0, n, tile) * nvec;
+  }
+  if (total > 0xffffffffLL - kConvThreads) return cudaErrorInvalidConfiguration;
+  const unsigned grid = unsigned((total + kConvThreads - 1) / kConvThreads);
+  dl_conv_prompt_kernel<T, VEC, W, SeqTable<NS>>
+      <<<grid, kConvThreads, 0, s>>>(p, tab, s0, unsigned(nvec), unsigned(total), tile);
   count_launches(1);
   return cudaGetLastError();
 }
 
-template <typename T, int VEC, int W, int TILE>
-cudaError_t conv_prompt_tiled(const ConvParams& p, int n, const int32_t* starts, cudaStream_t s) {
-  if (n <= kSmallSeqs) return conv_prompt_range<T, VEC, W, TILE, kSmallSeqs>(p, starts, 0, n, s);
+template <typename T, int VEC, int W>
+cudaError_t conv_prompt_t(const ConvParams& p, int n, const int32_t* starts, cudaStream_t s) {
+  if (n <= kSmallSeqs) return conv_prompt_range<T, VEC, W, kSmallSeqs>(p, starts, 0, n, s);
   for (int s0 = 0; s0 < n; s0 += kLargeSeqs) {
     const int m = n - s0 < kLargeSeqs ? n - s0 : kLargeSeqs;
-    const cudaError_t e = conv_prompt_range<T, VEC, W, TILE, kLargeSeqs>(p, starts, s0, m, s);
+    const cudaError_t e = conv_prompt_range<T, VEC, W, kLargeSeqs>(p, starts, s0, m, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 template <typename T, int VEC, int W>
-cudaError_t conv_prompt_t(const ConvParams& p, int n, const int32_t* starts, cudaStream_t s) {
-  return conv_prompt_tiled<T, VEC, W, 32>(p, n, starts, s);
-}
-
-template <typename T, int VEC, int W>
 cudaError_t conv_step_t(const ConvParams& p, int B, cudaStream_t s) {
   const int nvec = p.C / VEC;
-  const long long total = (long long)B * nvec;
-  const long long grid = (total + kConvThreads - 1) / kConvThreads;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  dl_conv_step_kernel<T, VEC, W><<<unsigned(grid), kConvThreads, 0, s>>>(p, nvec, total);
+  // as many sequences a thread as leave half a wave of threads, at most 8
+  long long rows = (long long)B * nvec / (one_wave() / 2);
+  rows = rows < 1 ? 1 : (rows > 8 ? 8 : rows);
+  const long long total = (B + rows - 1) / rows * nvec;
+  if (total > 0xffffffffLL - kConvThreads) return cudaErrorInvalidConfiguration;
+  const unsigned grid = unsigned((total + kConvThreads - 1) / kConvThreads);
+  dl_conv_step_kernel<T, VEC, W>
+      <<<grid, kConvThreads, 0, s>>>(p, B, unsigned(nvec), unsigned(total), int(rows));
   count_launches(1);
   return cudaGetLastError();
 }
@@ -235,7 +290,7 @@ cudaError_t by_width(int W, F&& f) {
 template <typename F>
 cudaError_t by_type(int W, bool bf16, bool vec, F&& f) {
   if (bf16)
-    return vec ? by_width<__nv_bfloat16, 8>(W, f) : by_width<__nv_bfloat16, 1>(W, f);
+    return vec ? by_width<__nv_bfloat16, 4>(W, f) : by_width<__nv_bfloat16, 1>(W, f);
   return vec ? by_width<float, 4>(W, f) : by_width<float, 1>(W, f);
 }
 

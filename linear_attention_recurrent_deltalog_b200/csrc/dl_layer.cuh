@@ -28,8 +28,7 @@ struct ConvParams {
   int silu;
 };
 
-// bf16: element type; vec: channels a thread covers with 16-byte accesses (1
-// when a pointer, a stride or C rules those out).
+// bf16: element type; vec: whether four channels can be accessed at a time.
 cudaError_t launch_conv_prompt(const ConvParams& p, int n, const int32_t* starts, int W, bool bf16,
                                bool vec, cudaStream_t s);
 cudaError_t launch_conv_step(const ConvParams& p, int B, int W, bool bf16, bool vec, cudaStream_t s);

@@ -24,12 +24,14 @@ int check_starts(int32_t n, const int32_t* starts) {
   return DL_OK;
 }
 
-int check_conv(const dl_conv_config* c, const void* x, int64_t ldx, const float* w,
+// Without rows (every sequence empty) x and y may be null.
+int check_conv(const dl_conv_config* c, bool rows, const void* x, int64_t ldx, const float* w,
                const float* bias, const void* h0, const void* h1, const void* y, int64_t ldy) {
   if (c == nullptr || c->C < 1 || c->W < 1 || !dtype_ok(c->in_dtype)) return DL_ERR_ARG;
   if ((c->flags & ~int32_t(DL_CONV_SILU)) != 0) return DL_ERR_ARG;
   if (c->W < 2 || c->W > 4) return DL_ERR_UNSUPPORTED;
-  if (!x || !w || !y || x == y || ldx < c->C || ldy < c->C) return DL_ERR_ARG;
+  if (!w || (rows && (!x || !y || x == y))) return DL_ERR_ARG;
+  if (ldx < c->C || ldy < c->C) return DL_ERR_ARG;
   if (h1 != nullptr && (h1 == x || h1 == y)) return DL_ERR_ARG;
   const size_t e = elem(c->in_dtype);
   if (!aligned(x, e) || !aligned(y, e) || !aligned(w, 4) || !aligned(bias, 4) || !aligned(h0, e) ||
@@ -38,11 +40,12 @@ int check_conv(const dl_conv_config* c, const void* x, int64_t ldx, const float*
   return DL_OK;
 }
 
-// Whether every row start the kernel touches is 16-byte aligned.
+// Whether four channels at a time can be read and written: rows, states and
+// C in units of four elements, taps and bias 16-byte aligned.
 bool conv_wide(const dl_conv_config& c, const dl::ConvParams& p) {
-  const size_t e = elem(c.in_dtype);
-  return aligned(p.x, 16) && aligned(p.y, 16) && aligned(p.h0, 16) && aligned(p.h1, 16) &&
-         (size_t(p.ldx) * e) % 16 == 0 && (size_t(p.ldy) * e) % 16 == 0 && (size_t(c.C) * e) % 16 == 0;
+  const size_t a = 4 * elem(c.in_dtype);
+  return aligned(p.x, a) && aligned(p.y, a) && aligned(p.h0, a) && aligned(p.h1, a) &&
+         aligned(p.w, 16) && aligned(p.bias, 16) && p.ldx % 4 == 0 && p.ldy % 4 == 0 && c.C % 4 == 0;
 }
 
 dl::ConvParams conv_params(const dl_conv_config& c, const void* x, int64_t ldx, const float* w,
@@ -70,10 +73,13 @@ int check_ssm(const dl_ssm_config* c) {
   return DL_OK;
 }
 
-int check_ssm_io(const dl_ssm_config& c, const dl_ssm_io* io) {
-  if (io == nullptr) return DL_ERR_ARG;
-  if (!io->q || !io->k || !io->v || !io->dt || !io->a || !io->o) return DL_ERR_ARG;
-  if (io->o == io->q || io->o == io->k || io->o == io->v) return DL_ERR_ARG;
+// Without rows (every sequence empty) their buffers may be null.
+int check_ssm_io(const dl_ssm_config& c, bool rows, const dl_ssm_io* io) {
+  if (io == nullptr || !io->a) return DL_ERR_ARG;
+  if (rows) {
+    if (!io->q || !io->k || !io->v || !io->dt || !io->o) return DL_ERR_ARG;
+    if (io->o == io->q || io->o == io->k || io->o == io->v) return DL_ERR_ARG;
+  }
   const int64_t nk = int64_t(c.G) * c.d_k, nv = int64_t(c.H) * c.d_v;
   if (io->ldq < nk || io->ldk < nk || io->ldv < nv || io->ldo < nv || io->lddt < c.H)
     return DL_ERR_ARG;
@@ -130,9 +136,9 @@ extern "C" {
 int dl_conv_prompt(const dl_conv_config* cfg, int32_t n, const int32_t* starts, const void* x,
                    int64_t ldx, const float* w, const float* bias, const void* h0, void* h1,
                    void* y, int64_t ldy, void* stream) {
-  int rc = check_conv(cfg, x, ldx, w, bias, h0, h1, y, ldy);
+  int rc = check_starts(n, starts);
   if (rc != DL_OK) return rc;
-  rc = check_starts(n, starts);
+  rc = check_conv(cfg, starts[n] > starts[0], x, ldx, w, bias, h0, h1, y, ldy);
   if (rc != DL_OK) return rc;
   if (n == 0) return DL_OK;
   const dl::ConvParams p = conv_params(*cfg, x, ldx, w, bias, h0, h1, y, ldy);
@@ -142,9 +148,9 @@ int dl_conv_prompt(const dl_conv_config* cfg, int32_t n, const int32_t* starts, 
 
 int dl_conv_step(const dl_conv_config* cfg, int32_t B, const void* x, int64_t ldx, const float* w,
                  const float* bias, void* h, void* y, int64_t ldy, void* stream) {
-  const int rc = check_conv(cfg, x, ldx, w, bias, h, h, y, ldy);
+  const int rc = check_conv(cfg, B > 0, x, ldx, w, bias, h, h, y, ldy);
   if (rc != DL_OK) return rc;
-  if (B < 0 || h == nullptr) return DL_ERR_ARG;
+  if (B < 0 || (B > 0 && h == nullptr)) return DL_ERR_ARG;
   if (B == 0) return DL_OK;
   const dl::ConvParams p = conv_params(*cfg, x, ldx, w, bias, h, h, y, ldy);
   return status(dl::launch_conv_step(p, B, cfg->W, cfg->in_dtype == DL_BF16, conv_wide(*cfg, p),
@@ -166,9 +172,10 @@ int dl_ssm_prompt(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, co
                   void* stream) {
   int rc = check_ssm(cfg);
   if (rc != DL_OK) return rc;
-  rc = check_ssm_io(*cfg, io);
-  if (rc != DL_OK) return rc;
   rc = check_starts(n, starts);
+  if (rc != DL_OK) return rc;
+  const bool rows = starts[n] > starts[0];
+  rc = check_ssm_io(*cfg, rows, io);
   if (rc != DL_OK) return rc;
   if (!aligned(S0, 16) || !aligned(S1, 16)) return DL_ERR_ALIGN;
   if (int64_t(n) * cfg->H > 0x7fffffff) return DL_ERR_ARG;
@@ -177,22 +184,22 @@ int dl_ssm_prompt(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, co
   if (!aligned(workspace, 256)) return DL_ERR_ALIGN;
   if (n == 0) return DL_OK;
   dl::SsmParams p = ssm_params(*cfg, *io, S0, S1);
-  if (cfg->in_dtype == DL_BF16) {
+  if (cfg->in_dtype == DL_BF16 && rows) {
     p.err = dl::shared_err_word();
     if (p.err == nullptr) return DL_ERR_CUDA;
     return status(dl::launch_ssm_chunked(p, n, starts, cfg->d_k, cfg->d_v, plan, workspace,
                                          static_cast<cudaStream_t>(stream)));
   }
-  return status(dl::launch_ssm_scan(p, n, starts, cfg->d_k, cfg->d_v, false,
+  return status(dl::launch_ssm_scan(p, n, starts, cfg->d_k, cfg->d_v, cfg->in_dtype == DL_BF16,
                                     static_cast<cudaStream_t>(stream)));
 }
 
 int dl_ssm_step(const dl_ssm_config* cfg, int32_t B, const dl_ssm_io* io, float* S, void* stream) {
   int rc = check_ssm(cfg);
   if (rc != DL_OK) return rc;
-  rc = check_ssm_io(*cfg, io);
+  rc = check_ssm_io(*cfg, B > 0, io);
   if (rc != DL_OK) return rc;
-  if (B < 0 || S == nullptr || int64_t(B) * cfg->H > 0x7fffffff) return DL_ERR_ARG;
+  if (B < 0 || (B > 0 && S == nullptr) || int64_t(B) * cfg->H > 0x7fffffff) return DL_ERR_ARG;
   if (!aligned(S, 16)) return DL_ERR_ALIGN;
   if (B == 0) return DL_OK;
   const dl::SsmParams p = ssm_params(*cfg, *io, S, S);
@@ -209,6 +216,7 @@ int dl_norm(const dl_norm_config* cfg, int64_t rows, const void* x, int64_t ldx,
   if (cfg->block != 0 && !(q && cfg->block == 128)) return DL_ERR_ARG;
   if (!(cfg->eps >= 0.f)) return DL_ERR_ARG;
   if (cfg->D > 16384) return DL_ERR_UNSUPPORTED;
+  if (rows == 0) return DL_OK;
   if (rows < 0 || !x || !w || !out || (q && scales == nullptr)) return DL_ERR_ARG;
   if (ldx < cfg->D || ldo < cfg->D || (res && ldr < cfg->D) || (res_out && ldro < cfg->D))
     return DL_ERR_ARG;
@@ -220,7 +228,6 @@ int dl_norm(const dl_norm_config* cfg, int64_t rows, const void* x, int64_t ldx,
   if (!aligned(x, e) || !aligned(res, e) || !aligned(res_out, e) || !aligned(w, 4) ||
       !aligned(out, eo) || !aligned(scales, 4))
     return DL_ERR_ALIGN;
-  if (rows == 0) return DL_OK;
   dl::NormParams p{};
   p.x = x;
   p.res = res;

@@ -3,10 +3,13 @@
 // written as fp32, bf16, or e4m3 codes with one fp32 scale per row or per
 // block of 128 channels (scale = amax / 448, code = e4m3(n * 448 / amax),
 // blocks below 2^-120 stored as zeros with scale 0).  Bound by HBM: x and
-// res are read once, res_out, the codes and the scales written once.  A team
-// of TPR threads owns a row and keeps it in registers (fp32) between the sum
-// of squares and the output; thread i takes 8 consecutive channels of each
-// TPR * 8, so a 128-channel block belongs to 16 neighbouring lanes.
+// res are read once, res_out, the codes and the scales written once.
+//
+// A team of TPR threads owns a row and keeps it in registers (fp32) between
+// the sum of squares and the output; a 128-channel block belongs to 16
+// neighbouring lanes, 8 channels each.  The grid holds as many teams as run
+// at once: each walks down the rows with its part of w in registers and the
+// next row's loads in flight while it finishes this one.
 #include <cuda_fp8.h>
 
 #include "dl_layer.cuh"
@@ -15,42 +18,78 @@ namespace dl {
 
 namespace {
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int left, bool vec, float (&v)[8]) {
-  if (vec) {
-    load_f<8>(p, v);
-    return;
-  }
+// Eight channels of a row as they lie in memory.  VEC: one or two 16-byte
+// accesses; else element by element, 16 channels apart, so that the 16 lanes
+// of a block touch neighbours.
+template <typename T, bool VEC>
+struct Raw8 {
+  T e[8];
+  __device__ __forceinline__ void load(const T* row, int c, int D) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = e < left ? to_f(p[e]) : 0.f;
-}
+    for (int i = 0; i < 8; ++i)
+      if (c + 16 * i < D) e[i] = row[c + 16 * i];
+  }
+  __device__ __forceinline__ float get(int i) const { return to_f(e[i]); }
+};
+template <>
+struct Raw8<__nv_bfloat16, true> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int c, int D) {
+    if (c < D) r = *reinterpret_cast<const uint4*>(row + c);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = i < 4 ? (i < 2 ? r.x : r.y) : (i < 6 ? r.z : r.w);
+    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+};
+template <>
+struct Raw8<float, true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* row, int c, int D) {
+    if (c < D) {
+      a = reinterpret_cast<const float4*>(row + c)[0];
+      b = reinterpret_cast<const float4*>(row + c)[1];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const float4 v = i < 4 ? a : b;
+    return (i & 2) ? ((i & 1) ? v.w : v.z) : ((i & 1) ? v.y : v.x);
+  }
+};
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int left, bool vec, const float (&v)[8]) {
-  if (vec) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(bf2(v[0], v[1]), bf2(v[2], v[3]), bf2(v[4], v[5]), bf2(v[6], v[7]));
-    return;
-  }
+// The same eight channels on the way out.
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int c, int D, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (c < D)
+      *reinterpret_cast<uint4*>(row + c) =
+          make_uint4(bf2(v[0], v[1]), bf2(v[2], v[3]), bf2(v[4], v[5]), bf2(v[6], v[7]));
+  } else {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < left) p[e] = __float2bfloat16_rn(v[e]);
-}
-__device__ __forceinline__ void store8(float* p, int left, bool vec, const float (&v)[8]) {
-  if (vec) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
+    for (int i = 0; i < 8; ++i)
+      if (c + 16 * i < D) row[c + 16 * i] = __float2bfloat16_rn(v[i]);
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < left) p[e] = v[e];
 }
-__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, int left, bool vec, const float (&v)[8]) {
+template <bool VEC>
+__device__ __forceinline__ void store8(float* row, int c, int D, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (c < D) {
+      reinterpret_cast<float4*>(row + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(row + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + 16 * i < D) row[c + 16 * i] = v[i];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_fp8_e4m3* row, int c, int D, const float (&v)[8]) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -60,14 +99,14 @@ __device__ __forceinline__ void store8(__nv_fp8_e4m3* p, int left, bool vec, con
                                                  __NV_SATFINITE, __NV_E4M3);
     w[i] = lo | (hi << 16);
   }
-  if (vec) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    return;
-  }
-  uint8_t* b = reinterpret_cast<uint8_t*>(p);
+  if constexpr (VEC) {
+    if (c < D) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+  } else {
+    uint8_t* b = reinterpret_cast<uint8_t*>(row);
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < left) b[e] = uint8_t(w[e >> 2] >> (8 * (e & 3)));
+    for (int i = 0; i < 8; ++i)
+      if (c + 16 * i < D) b[c + 16 * i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+  }
 }
 
 // The larger magnitude; a NaN on either side stays.
@@ -77,11 +116,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Sum or maximum over a team of TPR threads (whole warps).
+// Sum or maximum over a team of TPR threads: lanes of a warp, or a CTA.
 template <int TPR, bool MAX>
 __device__ __forceinline__ float team_reduce(float x, float* sm) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
     const float y = __shfl_xor_sync(0xffffffffu, x, o);
     x = MAX ? max_nan(x, y) : x + y;
   }
@@ -96,115 +135,130 @@ __device__ __forceinline__ float team_reduce(float x, float* sm) {
   return x;
 }
 
+template <int TPR>
+constexpr int kNormThreads = TPR < 128 ? 128 : TPR;
+
+// CTAs an SM must hold: 768 threads of 80 registers keep 48 KB of bf16 loads
+// in flight; fp32 rows (twice the bytes a thread) and odd ones take 128
+// registers and 512 threads.
+template <typename T, int TPR, bool VEC>
+constexpr int kNormCtas = (sizeof(T) == 2 && VEC ? 768 : 512) / kNormThreads<TPR>;
+
 template <typename T, typename TO, int TPR, int V, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(kNormThreads<TPR>, kNormCtas<T, TPR, VEC>)
 dl_norm_kernel(const NormParams p) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows a CTA covers
-  __shared__ float red[2][TPR / 32];
-  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
+  constexpr bool kCodes = std::is_same<TO, __nv_fp8_e4m3>::value;
+  constexpr int kRows = kNormThreads<TPR> / TPR;  // rows a CTA covers at a time
+  // two sets, used in turn: a thread may still read one when another writes the next row's
+  __shared__ float red[2][2][TPR / 32 + 1];
   const int i = threadIdx.x % TPR;
-  if (TPR == 32 && row >= p.rows) return;  // whole warps only
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + row * p.ldr : nullptr;
-  float h[V][8];
+  const int D = p.D;
+  int c[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) c[v] = VEC ? (v * TPR + i) * 8 : (v * TPR + (i & ~15)) * 8 + (i & 15);
+  const long long step = (long long)gridDim.x * kRows;
+  long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
+  // the row of the warp's first team: every lane takes the same turns
+  long long lead = TPR < 32 ? (long long)blockIdx.x * kRows + (threadIdx.x & ~31) / TPR : row;
+  Raw8<T, VEC> x[V], r[V];
+  auto fetch = [&](long long at) {
+    if (at >= p.rows) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v].load(static_cast<const T*>(p.x) + at * p.ldx, c[v], D);
+    if (p.res != nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) r[v].load(static_cast<const T*>(p.res) + at * p.ldr, c[v], D);
+    }
+  };
+  fetch(row);
+  float w[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = (v * TPR + i) * 8;
-    if (c < p.D) {
-      load8(x + c, p.D - c, VEC, h[v]);
-    } else {
+    Raw8<float, VEC> t;
+    t.load(p.w, c[v], D);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] = 0.f;
-    }
+    for (int e = 0; e < 8; ++e) w[v][e] = (VEC ? c[v] : c[v] + 16 * e) < D ? t.get(e) : 0.f;
   }
-  if (res != nullptr) {
-    float r[V][8];
+  const int nblk = p.block == 0 ? 1 : (D + 127) / 128;
+  for (int turn = 0; lead < p.rows; lead += step, row += step, turn ^= 1) {
+    const bool live = TPR >= 32 || row < p.rows;
+    float h[V][8];
+    float ss = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * TPR + i) * 8;
-      if (c < p.D) load8(res + c, p.D - c, VEC, r[v]);
-    }
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * TPR + i) * 8;
-      if (c < p.D) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[v][e] += r[v][e];
+      for (int e = 0; e < 8; ++e) {
+        float t = x[v].get(e);
+        if (p.res != nullptr) t += r[v].get(e);
+        h[v][e] = live && (VEC ? c[v] : c[v] + 16 * e) < D ? t : 0.f;
+        ss = fmaf(h[v][e], h[v][e], ss);
       }
+    fetch(row + step);
+    if (p.res_out != nullptr && live) {
+      T* ro = static_cast<T*>(p.res_out) + row * p.ldro;
+#pragma unroll
+      for (int v = 0; v < V; ++v) store8<VEC>(ro, c[v], D, h[v]);
     }
-  }
-  float ss = 0.f;
+    ss = team_reduce<TPR, false>(ss, red[turn][0]);
+    const float rn = 1.f / sqrtf(ss / float(D) + p.eps);
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(h[v][e], h[v][e], ss);
-  if (p.res_out != nullptr) {
-    T* ro = static_cast<T*>(p.res_out) + row * p.ldro;
+      for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * rn * w[v][e];
+    TO* out = static_cast<TO*>(p.out) + row * p.ldo;
+    if constexpr (kCodes) {
+      float m[V], rowmax = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * TPR + i) * 8;
-      if (c < p.D) store8(ro + c, p.D - c, VEC, h[v]);
-    }
-  }
-  ss = team_reduce<TPR, false>(ss, red[0]);
-  const float r = 1.f / sqrtf(ss / float(p.D) + p.eps);
-  float rowmax = 0.f;
+      for (int v = 0; v < V; ++v) {
+        m[v] = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = (v * TPR + i) * 8;
-    if (c >= p.D) continue;
-    float w[8];
-    load8(p.w + c, p.D - c, VEC, w);
+        for (int e = 0; e < 8; ++e) m[v] = max_nan(m[v], fabsf(h[v][e]));
+        rowmax = max_nan(rowmax, m[v]);
+      }
+      if (p.block == 0) {
+        rowmax = team_reduce<TPR, true>(rowmax, red[turn][1]);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * r * w[e];
-  }
-  TO* out = static_cast<TO*>(p.out) + row * p.ldo;
-  if constexpr (std::is_same<TO, __nv_fp8_e4m3>::value) {
-    float m[V];
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      m[v] = 0.f;
+          for (int o = 8; o > 0; o >>= 1) m[v] = max_nan(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
+      }
+      if (!live) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m[v] = max_nan(m[v], fabsf(h[v][e]));
-      rowmax = max_nan(rowmax, m[v]);
-    }
-    if (p.block == 0) {
-      rowmax = team_reduce<TPR, true>(rowmax, red[1]);
-    } else {
+      for (int v = 0; v < V; ++v) {
+        const float amax = p.block == 0 ? rowmax : m[v];
+        const bool zero = amax < kTinyAmax;
+        const float inv = zero ? 0.f : __fdiv_rn(448.f, amax);
+        const int first = VEC ? c[v] : c[v] - (i & 15) + (i & 15) * 8;  // as if it held 8 neighbours
+        if (p.block == 0 ? first == 0 : (first % 128 == 0 && first < D))
+          p.scales[row * nblk + (p.block == 0 ? 0 : first / 128)] = zero ? 0.f : __fdiv_rn(amax, 448.f);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+        for (int e = 0; e < 8; ++e) h[v][e] *= inv;
+        store8<VEC>(out, c[v], D, h[v]);
+      }
+    } else if (live) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m[v] = max_nan(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
-    }
-    const int nblk = p.block == 0 ? 1 : (p.D + 127) / 128;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * TPR + i) * 8;
-      if (c >= p.D) continue;
-      const float amax = p.block == 0 ? rowmax : m[v];
-      const bool zero = amax < kTinyAmax;
-      const float inv = zero ? 0.f : __fdiv_rn(448.f, amax);
-      if (p.block == 0 ? c == 0 : c % 128 == 0)
-        p.scales[row * nblk + (p.block == 0 ? 0 : c / 128)] = zero ? 0.f : __fdiv_rn(amax, 448.f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] *= inv;
-      store8(out + c, p.D - c, VEC, h[v]);
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * TPR + i) * 8;
-      if (c < p.D) store8(out + c, p.D - c, VEC, h[v]);
+      for (int v = 0; v < V; ++v) store8<VEC>(out, c[v], D, h[v]);
     }
   }
 }
 
 template <typename T, typename TO, int TPR, int V, bool VEC>
 cudaError_t norm_t(const NormParams& p, cudaStream_t s) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  const long long grid = (p.rows + kRows - 1) / kRows;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  dl_norm_kernel<T, TO, TPR, V, VEC><<<unsigned(grid), TPR < 128 ? 128 : TPR, 0, s>>>(p);
+  constexpr int kRows = kNormThreads<TPR> / TPR;
+  static std::atomic<int> per_sm{0};
+  auto kern = dl_norm_kernel<T, TO, TPR, V, VEC>;
+  int n = per_sm.load(std::memory_order_relaxed);
+  if (n == 0) {
+    const cudaError_t e =
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kNormThreads<TPR>, 0);
+    if (e != cudaSuccess) return e;
+    per_sm.store(n, std::memory_order_relaxed);
+  }
+  const long long most = (long long)n * sm_count();
+  if (most <= 0) return cudaErrorInvalidConfiguration;
+  const long long need = (p.rows + kRows - 1) / kRows;
+  kern<<<unsigned(need < most ? need : most), kNormThreads<TPR>, 0, s>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -212,11 +266,12 @@ cudaError_t norm_t(const NormParams& p, cudaStream_t s) {
 // The team and the 8-channel pieces a thread holds, by the row's length.
 template <typename T, typename TO, bool VEC>
 cudaError_t norm_by_length(const NormParams& p, cudaStream_t s) {
+  if (p.D <= 128) return norm_t<T, TO, 16, 1, VEC>(p, s);
   if (p.D <= 256) return norm_t<T, TO, 32, 1, VEC>(p, s);
-  if (p.D <= 1024) return norm_t<T, TO, 32, 4, VEC>(p, s);
+  if (p.D <= 512) return norm_t<T, TO, 32, 2, VEC>(p, s);
   if (p.D <= 2048) return norm_t<T, TO, 128, 2, VEC>(p, s);
-  if (p.D <= 4096) return norm_t<T, TO, 128, 4, VEC>(p, s);
-  if (p.D <= 8192) return norm_t<T, TO, 256, 4, VEC>(p, s);
+  if (p.D <= 4096) return norm_t<T, TO, 256, 2, VEC>(p, s);
+  if (p.D <= 8192) return norm_t<T, TO, 512, 2, VEC>(p, s);
   return norm_t<T, TO, 512, 4, VEC>(p, s);
 }
 

@@ -272,8 +272,9 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        if torch.cuda.is_available() and torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
+        if torch.cuda.is_initialized():
+            # the handle alone: current_stream() would build a Stream object per call
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         return None
     if isinstance(stream, int):
         return stream
@@ -282,9 +283,11 @@ def _stream(stream) -> Optional[int]:
 
 def _need(t, name: str, numel: int, dtype: torch.dtype) -> None:
     """Buffer checks that keep every kernel access inside the tensor."""
-    if t is None or isinstance(t, int):
+    if t is None:
         return
     if not isinstance(t, torch.Tensor):
+        if isinstance(t, int):
+            return
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -319,33 +322,35 @@ def _rows(t, name: str, rows: int, cols: int, dtype: torch.dtype) -> int:
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    shape = t.shape
+    shape, ld = t.shape, t.stride()
     if len(shape) == 2:
-        ok = shape[1] == cols and (cols == 1 or t.stride(1) == 1)
+        ok = shape[1] == cols and (ld[1] == 1 or cols == 1)
     else:
         ok = len(shape) == 3 and shape[1] * shape[2] == cols and \
             (shape[0] == 0 or t[0].is_contiguous())
     if not ok:
         raise ValueError(f"{name}: expected rows of {cols} contiguous elements, got shape "
-                         f"{tuple(shape)} with strides {t.stride()}")
+                         f"{tuple(shape)} with strides {ld}")
     if shape[0] < rows:
         raise ValueError(f"{name}: {shape[0]} rows, need {rows}")
     if shape[0] <= 1:
         return cols  # the one row's stride is never used
-    ld = t.stride(0)
-    if ld < cols:
-        raise ValueError(f"{name}: rows overlap (stride {ld}, {cols} elements)")
-    return ld
+    if ld[0] < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld[0]}, {cols} elements)")
+    return ld[0]
 
 
-def _on_device(tensors) -> None:
-    """Every tensor on the current CUDA device (whose stream the call uses)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in tensors:
-        if t is not None and not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if t is not None and (dev is None or t.get_device() != dev):
-            raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+def _on_device(names: str, *tensors) -> None:
+    """Every tensor (or None) on the current CUDA device, whose stream the call uses."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{names.split()[i]}: expected a torch.Tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{names.split()[i]}: must be on the current CUDA device, "
+                             f"not {t.device}")
 
 
 def _starts(starts):
@@ -433,7 +438,7 @@ def _conv_args(cfg: ConvConfig, rows: int, n: int, x, w, bias, h0, h1, y):
     _need(bias, "bias", cfg.C, torch.float32)
     _need(h0, "h0", n * (cfg.W - 1) * cfg.C, t)
     _need(h1, "h1", n * (cfg.W - 1) * cfg.C, t)
-    _on_device((("x", x), ("w", w), ("bias", bias), ("h0", h0), ("h1", h1), ("y", y)))
+    _on_device("x w bias h0 h1 y", x, w, bias, h0, h1, y)
     return ldx, ldy
 
 
@@ -477,8 +482,7 @@ def _ssm_io(cfg: SsmConfig, rows: int, n: int, q, k, v, dt, a, d, dt_bias, o, S0
         _need(x, name, H, torch.float32)
     _need(S0, "S0", n * nv * cfg.d_k, torch.float32)
     _need(S1, "S1", n * nv * cfg.d_k, torch.float32)
-    _on_device((("q", q), ("k", k), ("v", v), ("dt", dt), ("a", a), ("d", d),
-                ("dt_bias", dt_bias), ("o", o), ("S0", S0), ("S1", S1)))
+    _on_device("q k v dt a d dt_bias o S0 S1", q, k, v, dt, a, d, dt_bias, o, S0, S1)
     return dl_ssm_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), a.data_ptr(),
                      _ptr(d), _ptr(dt_bias), o.data_ptr(), *ld)
 
@@ -496,7 +500,7 @@ def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o,
     nb = workspace.numel() * workspace.element_size()
     if not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
-    _on_device((("workspace", workspace),))
+    _on_device("workspace", workspace)
     _check(_lib.dl_ssm_prompt(ctypes.byref(cfg.c), n, arr.ctypes.data, ctypes.byref(io), _ptr(S0),
                               _ptr(S1), workspace.data_ptr() if nb else None, nb,
                               _stream(stream)), "dl_ssm_prompt")
@@ -527,8 +531,7 @@ def dl_norm(cfg: NormConfig, x, w, out, res=None, res_out=None, scales=None, str
     if cfg.out_dtype == "e4m3" and scales is None:
         raise TypeError("scales: expected a torch.Tensor for an e4m3 output")
     _need(scales, "scales", rows * cfg.scales_per_row, torch.float32)
-    _on_device((("x", x), ("w", w), ("out", out), ("res", res), ("res_out", res_out),
-                ("scales", scales)))
+    _on_device("x w out res res_out scales", x, w, out, res, res_out, scales)
     _check(_lib.dl_norm(ctypes.byref(cfg.c), rows, x.data_ptr(), ldx, _ptr(res), ldr, w.data_ptr(),
                         _ptr(res_out), ldro, out.data_ptr(), ldo, _ptr(scales), _stream(stream)),
            "dl_norm")

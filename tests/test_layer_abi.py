@@ -183,3 +183,18 @@ def test_binding_checks_tensors():
             dl.dl_ssm_step(s, **{**args, name: bad})
     with pytest.raises(ValueError, match="current CUDA device"):
         dl.dl_ssm_step(s, **args)
+
+
+def test_calls_without_rows_need_no_row_buffers():
+    conv, ssm = dl.ConvConfig(64, 4), dl.SsmConfig(4, 2, 64, 64)
+    assert conv_prompt(conv, starts(0), x=None, y=None) == dl.DL_OK
+    assert conv_prompt(conv, starts(0), x=None, y=None, w=None) == dl.DL_ERR_ARG
+    assert lib.dl_conv_step(ctypes.byref(conv.c), 0, None, 64, Q, None, None, None, 64, None) == dl.DL_OK
+    x = io(ssm, q=None, k=None, v=None, dt=None, o=None)
+    c, xp, st = ctypes.byref(ssm.c), ctypes.byref(x), starts(3)
+    assert lib.dl_ssm_step(c, 0, xp, None, None) == dl.DL_OK
+    assert lib.dl_ssm_step(c, 1, xp, P, None) == dl.DL_ERR_ARG
+    assert lib.dl_ssm_prompt(c, 0, st.ctypes.data, xp, None, None, None, 0, None) == dl.DL_OK
+    x = io(ssm, a=None)
+    assert lib.dl_ssm_step(c, 0, ctypes.byref(x), None, None) == dl.DL_ERR_ARG
+    assert norm(dl.NormConfig(64), rows=0, x=None, out=None) == dl.DL_OK

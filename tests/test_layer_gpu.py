@@ -433,6 +433,31 @@ def test_prompt_in_a_graph_and_twice_the_same():
         assert torch.equal(o, outs[0][0]) and torch.equal(s, outs[0][1])
 
 
+# ------------------------------------------------------------ empty calls
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_without_rows(dtype):
+    # empty batches do nothing; prompts of no tokens pass their states on
+    t = DT[dtype]
+    z = lambda *s: torch.zeros(*s, dtype=t, device="cuda")
+    f = lambda *s: torch.zeros(*s, device="cuda")
+    dl.dl_norm(dl.NormConfig(64, dtype, "e4m3"), z(0, 64), f(64),
+               z(0, 64).to(torch.float8_e4m3fn), scales=f(0, 1))
+    conv = dl.ConvConfig(24, 4, dtype)
+    dl.dl_conv_step(conv, z(0, 24), f(24, 4), None, z(0, 3, 24), z(0, 24))
+    h0, h1 = rnd(1, 2, 3, 24).to(t).cuda(), z(2, 3, 24)
+    dl.dl_conv_prompt(conv, [0, 0, 0], z(0, 24), f(24, 4), None, h0, h1, z(0, 24))
+    assert torch.equal(h0, h1)
+    ssm = dl.SsmConfig(2, 1, 64, 128, dtype)
+    row = (z(0, 64), z(0, 64), z(0, 256), f(0, 2), f(2) - 1, None, None)
+    dl.dl_ssm_step(ssm, *row, f(0, 2, 128, 64), z(0, 256))
+    S0, S1 = rnd(2, 2, 2, 128, 64).cuda(), f(2, 2, 128, 64)
+    dl.dl_ssm_prompt(ssm, [0, 0, 0], *row, S0, S1, z(0, 256))
+    assert torch.equal(S0, S1)
+    dl.dl_ssm_prompt(ssm, [0, 0, 0], *row, None, S1, z(0, 256))
+    assert (S1 == 0).all()
+
+
 # --------------------------------------------------- the operators together
 
 def test_prompt_then_tokens_as_one_layer():
