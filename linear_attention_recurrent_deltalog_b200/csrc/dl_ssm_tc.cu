@@ -11,13 +11,13 @@
 // accumulators in TMEM):
 //     G = Q K^T            [t, i]   A, B from shared memory, K-major
 //     Y = Q S^T            [t, p]   B: the state as bf16, written by its owners
-//     Z = M V              [t, p]   A: M as bf16 in TMEM, B: V, MN-major
-//     D = K^T (w o V)      [n, p]   A: K, MN-major, B: w o V in three bf16 parts
-// Rounding: the state is carried in fp32 registers (one thread per key
-// channel and 64 value rows) and w o V enters D as hi + mid + lo, all 24 bits,
-// so S' is right to fp32 rounding; only what feeds the bf16 output o is rounded
-// to bf16 on the way, each term once (M, or the state that q reads), which
-// is of the size of o's own rounding.
+//     Y = grow o Y + M V   [t, p]   A: M as bf16 in TMEM, B: V, MN-major
+//     D = (w o V)^T K      [p, n]   A: w o V in TMEM as three bf16 parts, B: K, MN-major
+// Rounding: the state is carried in fp32 registers (one thread per value
+// row) and w o V enters D as hi + mid + lo, all 24
+// bits, so S' is right to fp32 rounding; only what feeds the bf16 output o is
+// rounded to bf16 on the way, each term once (M, or the state that q reads),
+// which is of the size of o's own rounding.
 //
 // A CTA owns 128 value columns (two neighbouring heads of a group at d_v = 64,
 // which share G and the loads of q and k; one head at 128) and walks the
@@ -26,12 +26,18 @@
 // from zero, dl_ssm_join_kernel turns those into the state each tile enters
 // with, and the main launch starts from them.
 //
-// Warps 0-7: element work on M, the state and o (warp w reaches TMEM lanes
-// 32 (w mod 4) ..; w / 4 picks the 64 value columns).  Warps 8-11: w o V, 16
-// tokens at a time.  Warp 12: TMA.  Warp 13: MMA issue.  Warps 14, 15: dt,
-// decays and their sums, one chunk ahead.  In turn the tensor cores run
-// G, Y, D, Z = M V of a chunk; M is formed while Y and D run, the state moves on
-// and o is written while Z and the next G run.
+// What bounds a chunk is shared memory (an MMA with both operands there reads
+// 128 bytes a cycle, all it can deliver), which is why M and w o V are TMEM
+// operands: with w o V in shared memory its parts were written once and read,
+// with K, three times over, 0.3 MB more a chunk.
+//
+// Warps 0-7: M and o (warp w reaches TMEM lanes 32 (w mod 4) ..).  Warps 8-11:
+// the state, a value row a thread.  Warps 12-19: w o V, 16 tokens at a time.
+// Warp 20: TMA.  Warp 21: MMA issue.  Warps 22, 23: dt, decays and their sums,
+// one chunk ahead.  In turn the tensor cores run G, D with Y in its middle,
+// M V; M is formed while D runs, the state moves on and o is written while M V
+// and the next G run.  (With the state and M in the same warps, one after the
+// other, a chunk took half as long again.)
 #include <cuda.h>
 
 #include "dl_layer.cuh"
@@ -42,8 +48,10 @@ namespace dl {
 namespace {
 
 constexpr int kQ = 128;             // tokens per chunk
-constexpr int kThreads = 512;
-constexpr int kElemWarps = 8, kWeighWarps = 4;
+constexpr int kElemWarps = 8, kStateWarps = 4, kWeighWarps = 8, kCtrlWarps = 4;
+constexpr int kFirstState = kElemWarps, kFirstWeigh = kFirstState + kStateWarps,
+              kFirstCtrl = kFirstWeigh + kWeighWarps;
+constexpr int kThreads = 32 * (kFirstCtrl + kCtrlWarps);
 constexpr int kPiece = 16;          // tokens of w o V staged at a time
 constexpr int kPieces = kQ / kPiece;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -51,40 +59,40 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLambda = -150.f;
 
 // TMEM columns.  M takes G's place block by block: tokens 32 b .. 32 b + 31 of
-// head slot s are the 16 columns at kColG + 32 b + 16 s.
-constexpr uint32_t kColG = 0, kColY = 128, kColZ = 256, kColD = 384;
+// head slot s are the 16 columns at kColG + 32 b + 16 s.  A stage of w o V is
+// three parts of 8 columns (16 tokens, two a column).
+constexpr int kStages = 4;
+constexpr uint32_t kColG = 0, kColY = 128, kColW = 256, kColD = 384;
+constexpr uint32_t kWPart = kPiece / 2, kWStage = 3 * kWPart;
+static_assert(kColW + kStages * kWStage <= kColD, "TMEM columns");
 
 template <int DK>
 struct TcLayout {
-  static constexpr uint32_t kKBlocks = DK / 64;                 // 64-column boxes of q and k
+  static constexpr uint32_t kKBlocks = DK / 64;                 // 64-column boxes of q, k and the state
   static constexpr uint32_t kBox = kQ * 128;                    // bytes of a box
   static constexpr uint32_t kK = kKBlocks * kBox;
   static constexpr uint32_t offQ = 0;
   static constexpr uint32_t offK = offQ + kK;                   // two stages
   static constexpr uint32_t offV = offK + 2 * kK;               // two stages of two boxes
-  static constexpr uint32_t offW = offV + 4 * kBox;             // two stages x 3 parts x 2 boxes x 16 rows
-  static constexpr uint32_t kWBox = kPiece * 128;
-  static constexpr uint32_t kWPart = 2 * kWBox;
-  static constexpr uint32_t kWStage = 3 * kWPart;
-  static constexpr uint32_t offS = offW + 2 * kWStage;          // 2 boxes of DK rows
-  static constexpr uint32_t kSBox = DK * 128;
+  static constexpr uint32_t offS = offV + 4 * kBox;             // the state, 128 value rows
   // per token, [2 buffers][2 heads][128] floats: s, dt, w; and the column
   // factors of M's blocks below the diagonal ones, 32 + 64 + 96 per head
-  static constexpr uint32_t offF = offS + 2 * kSBox;
+  static constexpr uint32_t offF = offS + kK;
   static constexpr uint32_t kF = 2 * 2 * kQ * 4;
   static constexpr uint32_t kCols = 192;
   static constexpr uint32_t offC = offF + 3 * kF;
   static constexpr uint32_t offT = offC + 2 * 2 * kCols * 4;    // tot [2][2]
   static constexpr uint32_t offBar = offT + 16;
-  static constexpr uint32_t total = offBar + 32 * 8 + 16 + 1024;  // + alignment of the base
+  static constexpr uint32_t total = offBar + 40 * 8 + 16 + 1024;  // + alignment of the base
 };
 static_assert(TcLayout<128>::total <= kMaxSmemOptIn, "shared memory of a CTA");
 
 enum Bar {
-  kFullQ, kFullK0, kFullK1, kFullV0, kFullV1, kWts0, kWts1, kWtsFree0, kWtsFree1, kWFull0, kWFull1,
-  kWFree0, kWFree1, kG, kY, kD0, kD1, kZ0, kZ1, kMReady, kSReady, kYFree0, kYFree1,
-  kPair0, kPair1, kPair2, kPair3, kBars
+  kFullQ, kFullK0, kFullK1, kFullV0, kFullV1, kWts0, kWts1, kWtsFree0, kWtsFree1, kWFull0,
+  kWFree0 = kWFull0 + kStages, kG = kWFree0 + kStages, kY, kD0, kD1, kZ0, kZ1, kMReady, kSReady, kSReady1,
+  kYFree, kVFree0, kVFree1, kPair0, kBars = kPair0 + 4
 };
+static_assert(kBars <= 40, "barrier slots");
 
 struct TcParams {
   const float* dt;
@@ -94,7 +102,7 @@ struct TcParams {
   const float* S0;
   float* S1;
   __nv_bfloat16* o;
-  float* ws;        // [tiles, H, DV, DK]: STATES writes a tile's own state, main reads its entry state
+  float* ws;        // [tiles, H, DK, DV]: STATES writes a tile's own state, main reads its entry state
   float* wdecay;    // [tiles, H] log2 of a tile's whole decay
   int* err;
   long long lddt, ldo;
@@ -109,6 +117,21 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// x below the diagonal (j < lane), x + d on it, 0 above.  In assembly, because
+// the compiler would branch around the exponential in x, once an element.
+__device__ __forceinline__ float on_diagonal(float x, float d, int j, int lane) {
+  float r;
+  asm("{\n\t.reg .pred p, q;\n\t.reg .f32 y;\n\t"
+      "setp.eq.s32 p, %3, %4;\n\t"
+      "setp.gt.s32 q, %3, %4;\n\t"
+      "selp.f32 y, %2, 0f00000000, p;\n\t"
+      "add.rn.f32 y, y, %1;\n\t"
+      "selp.f32 %0, 0f00000000, y, q;\n\t}"
+      : "=f"(r)
+      : "f"(x), "f"(d), "r"(j), "r"(lane));
+  return r;
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
   asm volatile(
@@ -116,6 +139,17 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       "%3}], [%4];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
+}
+
+// A box of 32 rows on its way out, and the wait until its shared memory has been read.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // Descriptors of 128-byte swizzled operands: boxes of 128-byte rows (64 bf16).
@@ -186,45 +220,92 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// 16 lanes x 32 columns: registers 4 b + 2 i, + 1 of lane l are columns 8 b +
+// 2 (l mod 4), + 1 of TMEM lane 8 i + l / 4.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// mbar_wait with a long suspension: a waiting warp sleeps until its phase
+// completes (or a millisecond has passed) and leaves the issue slots to others.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* err, int head) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (done) return true;
+    if (clock64() - t0 > kWaitCycles) {
+      if (err != nullptr && atomicCAS(err, 0, kDevErrTimeout) == 0) err[1] = head;
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ uint32_t pack_bf(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
+// Two bf16 values times two weights, each product as three bf16 parts whose
+// sum is the fp32 product: the upper 16 bits are cut off twice (exact
+// remainders), the last part is rounded.  21 cycles a scheduler; products and
+// remainders in packed bf16 operations took 40, in packed fp32 ones no less.
+__device__ __forceinline__ void weigh2(uint32_t v2, float2 w, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  float a = __uint_as_float(v2 << 16) * w.x, b = __uint_as_float(v2 & 0xffff0000u) * w.y;
+  hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+  b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+  mid = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+  b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+  lo = pack_bf(a, b);
 }
 
-// Eight bf16 (two per word) times w, each product as three bf16 parts whose
-// sum is the fp32 product: the upper 16 bits are cut off twice (exact
-// remainders), the last part is rounded.
-__device__ __forceinline__ void weigh8(uint4 x, float w, uint4& hi, uint4& mid, uint4& lo) {
-  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-  uint32_t o0[4], o1[4], o2[4];
-  const uint64_t w2 = f2_pack(w, w), minus = f2_pack(-1.f, -1.f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    const uint64_t y =
-        f2_mul(f2_pack(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), w2);
-    f2_unpack(y, a, b);
-    o0[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-    const uint64_t r = f2_fma(f2_pack(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
-                                      __uint_as_float(__float_as_uint(b) & 0xffff0000u)),
-                              minus, y);
-    f2_unpack(r, a, b);
-    o1[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-    const uint64_t r2 = f2_fma(f2_pack(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
-                                       __uint_as_float(__float_as_uint(b) & 0xffff0000u)),
-                               minus, r);
-    f2_unpack(r2, a, b);
-    o2[i] = pack_bf(a, b);
-  }
-  hi = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-  mid = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-  lo = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+// Four 8 x 8 matrices of 16-bit elements, transposed: register m of lane l
+// holds rows 2 (l mod 4), 2 (l mod 4) + 1 of column l / 4 of matrix m.
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t (&r)[4], const void* row_addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(row_addr))
+               : "memory");
+}
+// 16 lanes x 8 columns: registers 0, 1 (2, 3) of lane l are column l mod 4 (4 +
+// l mod 4) of TMEM lanes l / 4 and 8 + l / 4.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
 template <int N>
@@ -235,10 +316,11 @@ template <int N>
 __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// 8 element warps of 168, 4 of 96, 4 of 72: 64,512 of the 65,536 the block starts with (128 each).
-constexpr int kElemRegs = 168, kWeighRegs = 96, kCtrlRegs = 72;
-static_assert(kElemWarps * 32 * kElemRegs + kWeighWarps * 32 * kWeighRegs + 4 * 32 * kCtrlRegs <=
-                  kThreads * 128,
+// Registers a thread starts with, and the share of each role.
+constexpr int kStartRegs = 80, kElemRegs = 88, kStateRegs = 168, kWeighRegs = 48, kCtrlRegs = 40;
+static_assert(kElemWarps * kElemRegs + kStateWarps * kStateRegs + kWeighWarps * kWeighRegs +
+                      kCtrlWarps * kCtrlRegs <=
+                  kThreads / 32 * kStartRegs,
               "register shares");
 
 // One arrival per warp once all its lanes are done.
@@ -252,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int seq0,
                     const __grid_constant__ CUtensorMap mapQ,
                     const __grid_constant__ CUtensorMap mapK,
-                    const __grid_constant__ CUtensorMap mapV) {
+                    const __grid_constant__ CUtensorMap mapV,
+                    const __grid_constant__ CUtensorMap mapO) {
   using L = TcLayout<DK>;
   constexpr int kHeads = 128 / DV;  // heads a CTA covers
   extern __shared__ unsigned char smem_raw[];
@@ -261,7 +344,6 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
   unsigned char* sQ = smem + L::offQ;
   unsigned char* sK = smem + L::offK;
   unsigned char* sV = smem + L::offV;
-  unsigned char* sW = smem + L::offW;
   unsigned char* sS = smem + L::offS;
   float* fS = reinterpret_cast<float*>(smem + L::offF);  // [buf][head][token]
   float* fDt = fS + 2 * 2 * kQ;
@@ -269,7 +351,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
   float* fC = reinterpret_cast<float*>(smem + L::offC);
   float* fT = reinterpret_cast<float*>(smem + L::offT);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::offBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 40);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -296,10 +378,11 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     for (int i = 0; i < kBars; ++i) {
       uint32_t n = 1;
       if (i == kWts0 || i == kWts1) n = kHeads;
-      if (i == kWtsFree0 || i == kWtsFree1) n = kElemWarps + kWeighWarps;
-      if (i == kWFull0 || i == kWFull1) n = kWeighWarps;
+      if (i == kWtsFree0 || i == kWtsFree1) n = (STATES ? 0 : kElemWarps) + kStateWarps + kWeighWarps;
+      if (i == kSReady || i == kSReady1) n = kStateWarps;
+      if (i >= kWFull0 && i < kWFree0) n = kWeighWarps / 2;
       if (i >= kPair0) n = 2;
-      if (i == kMReady || i == kSReady || i == kYFree0 || i == kYFree1) n = kElemWarps;
+      if (i == kMReady || i == kYFree || i == kVFree0 || i == kVFree1) n = kElemWarps;
       mbar_init(&bars[i], n);
     }
     fence_mbar_init();
@@ -312,19 +395,19 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
   const int errh = int(seq) * p.H + h0;
 // One thread's wait, and a whole warp's (which gives up as one).
 #define DL_WAIT(bar, parity)                            \
-  if (!mbar_wait(&bars[bar], (parity), p.err, errh)) { \
+  if (!wait_phase(&bars[bar], (parity), p.err, errh)) { \
     *abort_flag = 1;                                    \
     goto done;                                          \
   }
 #define DL_WAIT_WARP(bar, parity)                                               \
-  if (!__all_sync(0xffffffffu, mbar_wait(&bars[bar], (parity), p.err, errh))) { \
+  if (!__all_sync(0xffffffffu, wait_phase(&bars[bar], (parity), p.err, errh))) { \
     *abort_flag = 1;                                                            \
     goto done;                                                                  \
   }
 
-  if (warp >= 12) {
+  if (warp >= kFirstCtrl) {
     give_registers<kCtrlRegs>();
-    if (warp == 12) {
+    if (warp == kFirstCtrl) {
       // ----------------------------------------------------------- copies
       if (lane == 0) {
         auto copy = [&](unsigned char* dst, const CUtensorMap* map, uint32_t boxes, int x, int c, int bar) {
@@ -340,28 +423,29 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
           copy_k(c);
           copy_v(c);
         }
-        for (int c = 0; c + 1 < nch; ++c) {  // each buffer's last reader belongs to chunk c
+        // in the order in which a chunk sets buffers free: the values' (an output's
+        // on its way out, or w o V's source) and q at once, k for the next but one
+        for (int c = 0; c + 1 < nch; ++c) {
+          if (c > 0) {
+            if (!STATES) DL_WAIT(kVFree0 + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+            copy_v(c + 1);
+          }
           if (!STATES) {
             DL_WAIT(kY, c & 1);
             copy_q(c + 1);
           }
-          if (c + 2 < nch) {
-            DL_WAIT(kD0 + (c & 1), (c >> 1) & 1);
-            copy_k(c + 2);
-            // chunk c's values made room for its outputs on their way out
-            if (!STATES) DL_WAIT(kYFree0 + (c & 1), (c >> 1) & 1);
-            copy_v(c + 2);
-          }
+          DL_WAIT(kD0 + (c & 1), (c >> 1) & 1);
+          if (c + 2 < nch) copy_k(c + 2);
         }
       }
-    } else if (warp == 13) {
+    } else if (warp == kFirstCtrl + 1) {
       // ------------------------------------------------------------- MMAs
       {
         const uint32_t lead = elect_lane();
         constexpr uint32_t idG = idesc_bf16(128, 128, false, false);
-        constexpr uint32_t idY = idesc_bf16(128, 128, false, true);
+        constexpr uint32_t idY = idG;
         constexpr uint32_t idM = idesc_bf16(128, DV == 64 ? 64 : 128, false, true);
-        constexpr uint32_t idD = idesc_bf16(128, 128, true, true);
+        constexpr uint32_t idD = idesc_bf16(128, DK, false, true);
         for (int c = 0; c < nch; ++c) {
           const uint32_t ph = uint32_t(c) & 1u;
           const unsigned char* k = sK + ph * L::kK;
@@ -376,27 +460,31 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
               umma_ss(lead, tmem + kColG, desc_sw128(sQ + (ks / 4) * L::kBox + (ks % 4) * 32, 16),
                        desc_sw128(k + (ks / 4) * L::kBox + (ks % 4) * 32, 16), idG, ks > 0);
             umma_done(lead, &bars[kG]);
-            if (c > 0) DL_WAIT_WARP(kYFree0 + ((c - 1) & 1), ((c - 1) >> 1) & 1);
           }
-          DL_WAIT_WARP(kSReady, ph);
+          // STATES alternates between two accumulators (no G takes the other's
+          // place): chunk c waits for the state to have taken up c - 2
+          if (!STATES) DL_WAIT_WARP(kSReady, ph);
+          if (STATES && c > 1) DL_WAIT_WARP(kSReady + ph, ((c >> 1) - 1) & 1);
           tc_fence_after();
-          if (!STATES) {
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks)
-              umma_ss(lead, tmem + kColY, desc_sw128(sQ + (ks / 4) * L::kBox + (ks % 4) * 32, 16),
-                       desc_sw128(sS + ks * 2048, L::kSBox), idY, ks > 0);
-            umma_done(lead, &bars[kY]);
-          }
+          const uint32_t dcol = tmem + (STATES && ph ? kColG : kColD);
 #pragma unroll 1
           for (int pc = 0; pc < kPieces; ++pc) {
-            const int st = pc & 1;
-            DL_WAIT_WARP(kWFull0 + st, (c * (kPieces / 2) + (pc >> 1)) & 1);
+            if (!STATES && pc == kPieces / 2) {  // by now the last chunk's Y has been read
+              if (c > 0) DL_WAIT_WARP(kYFree, (c - 1) & 1);
+              tc_fence_after();
+#pragma unroll
+              for (int ks = 0; ks < DK / 16; ++ks)
+                umma_ss(lead, tmem + kColY, desc_sw128(sQ + (ks / 4) * L::kBox + (ks % 4) * 32, 16),
+                        desc_sw128(sS + (ks / 4) * L::kBox + (ks % 4) * 32, 16), idY, ks > 0);
+              umma_done(lead, &bars[kY]);
+            }
+            const int st = pc % kStages;
+            DL_WAIT_WARP(kWFull0 + st, (c * (kPieces / kStages) + pc / kStages) & 1);
             tc_fence_after();
-            const uint64_t a = desc_sw128(k + pc * (kPiece * 128), L::kBox);
+            const uint64_t kd = desc_sw128(k + pc * (kPiece * 128), L::kBox);
 #pragma unroll
             for (int part = 0; part < 3; ++part)
-              umma_ss(lead, tmem + kColD, a, desc_sw128(sW + st * L::kWStage + part * L::kWPart, L::kWBox), idD,
-                       pc + part > 0);
+              umma_ts(lead, dcol, tmem + kColW + st * kWStage + part * kWPart, kd, idD, pc + part > 0);
             umma_done(lead, &bars[kWFree0 + st]);
           }
           umma_done(lead, &bars[kD0 + ph]);
@@ -407,15 +495,15 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
             for (int hd = 0; hd < kHeads; ++hd)
 #pragma unroll
               for (int ks = 0; ks < kQ / 16; ++ks)
-                umma_ts(lead, tmem + kColZ + hd * 64, tmem + kColG + (ks >> 1) * 32 + hd * 16 + (ks & 1) * 8,
-                        desc_sw128(v + hd * L::kBox + ks * 2048, L::kBox), idM, ks > 0);
+                umma_ts(lead, tmem + kColY + hd * 64, tmem + kColG + (ks >> 1) * 32 + hd * 16 + (ks & 1) * 8,
+                        desc_sw128(v + hd * L::kBox + ks * 2048, L::kBox), idM, true);
             umma_done(lead, &bars[kZ0 + ph]);
           }
         }
       }
     } else {
       // ----------------------------------------------------------- decays
-      const int hs = warp - 14;
+      const int hs = warp - kFirstCtrl - 2;
       const int h = h0 + hs;
       if (hs < kHeads) {
         const bool live = h < hend;
@@ -481,250 +569,325 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
         }
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= kFirstWeigh) {
     // -------------------------------------------------------------- w o V
     give_registers<kWeighRegs>();
-    const int t = tid - kElemWarps * 32;               // 0 .. 127
-    const int box = t >> 6, r = (t >> 3) & 7, off = r * 128 + (t & 7) * 16;
+    const int odd = (warp - kFirstWeigh) >> 2;  // four warps take the even pieces, four the odd ones
+    const int quarter = warp & 3;
+    const uint32_t lanes = uint32_t(quarter * 32) << 16;
+    const int head = DV == 64 ? quarter >> 1 : 0;
+    // this lane's row of the matrices it points at: tokens r, 8 + r; 8 value columns each
+    const int r = lane & 7, trow = (lane >> 4) * 8 + r, pblk = (lane >> 3) & 1;
+    uint32_t at[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      at[i] = (quarter >> 1) * L::kBox + trow * 128 + ((((quarter & 1) * 4 + i * 2 + pblk) ^ r) << 4);
     for (int c = 0; c < nch; ++c) {
       const int buf = c & 1;
       const int len = min(kQ, end - (begin + c * kQ));
       unsigned char* v = sV + buf * 2 * L::kBox;
-      const float* w = fW + (buf * 2 + (DV == 64 ? box : 0)) * kQ;
+      const float2* w = reinterpret_cast<const float2*>(fW + (buf * 2 + head) * kQ) + (lane & 3);
       DL_WAIT_WARP(kWts0 + buf, (c >> 1) & 1);
       DL_WAIT_WARP(kFullV0 + buf, (c >> 1) & 1);
-      if (len < kQ) {
+      if (len < kQ && odd == 0) {
         // rows behind the sequence may hold anything: zeros for the sums over
-        // tokens (G's columns there are masked)
+        // tokens (G's columns there are masked), in place before the first piece
         DL_WAIT_WARP(kFullK0 + buf, (c >> 1) & 1);
-        for (int i = t; i < (kQ - len) * 8; i += kWeighWarps * 32) {
+        for (int i = tid - kFirstWeigh * 32; i < (kQ - len) * 8; i += 128) {
           const int at = (len + (i >> 3)) * 128 + (i & 7) * 16;
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
           for (uint32_t b = 0; b < L::kKBlocks; ++b)
             *reinterpret_cast<uint4*>(sK + buf * L::kK + b * L::kBox + at) = zero;
           for (uint32_t b = 0; b < 2; ++b) *reinterpret_cast<uint4*>(v + b * L::kBox + at) = zero;
         }
+        fence_async_smem();
       }
 #pragma unroll 1
-      for (int pc = 0; pc < kPieces; ++pc) {
-        const int st = pc & 1, use = c * (kPieces / 2) + (pc >> 1);
-        uint4 x[2];
-        float wt[2];
+      for (int pc = odd; pc < kPieces; pc += 2) {
+        const int st = pc % kStages, use = c * (kPieces / kStages) + pc / kStages;
+        uint32_t x[2][4], part[3][2][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = pc * kPiece + 8 * j + r;
-          x[j] = *reinterpret_cast<const uint4*>(v + box * L::kBox + pc * (kPiece * 128) + j * 1024 + off);
-          wt[j] = w[row];
-          if (row >= len) x[j] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 2; ++i) ldmatrix_x4_t(x[i], v + pc * (kPiece * 128) + at[i]);
+        const float2 w0 = w[pc * (kPiece / 2)], w1 = w[pc * (kPiece / 2) + 4];
+        if ((pc + 1) * kPiece > len) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int first = pc * kPiece + (j >> 1) * 8 + 2 * (lane & 3);
+            const uint32_t keep = first >= len ? 0u : (first + 1 >= len ? 0xffffu : 0xffffffffu);
+            x[0][j] &= keep;
+            x[1][j] &= keep;
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            weigh2(x[i][j], j < 2 ? w0 : w1, part[0][i][j], part[1][i][j], part[2][i][j]);
         if (use > 0) DL_WAIT_WARP(kWFree0 + st, (use - 1) & 1);
-        unsigned char* dst = sW + st * L::kWStage + box * L::kWBox + off;
+        tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint4 hi, mid, lo;
-          weigh8(x[j], wt[j], hi, mid, lo);
-          *reinterpret_cast<uint4*>(dst + j * 1024) = hi;
-          *reinterpret_cast<uint4*>(dst + L::kWPart + j * 1024) = mid;
-          *reinterpret_cast<uint4*>(dst + 2 * L::kWPart + j * 1024) = lo;
-        }
-        fence_async_smem();
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            tmem_st_16x8(tmem + kColW + st * kWStage + n * kWPart + lanes + (uint32_t(16 * i) << 16), part[n][i]);
+        tmem_wait_st();
+        tc_fence_before();
         warp_arrive(&bars[kWFull0 + st], lane);
       }
       warp_arrive(&bars[kWtsFree0 + buf], lane);
     }
-  } else {
-    // ------------------------------------------------------- element work
-    take_registers<kElemRegs>();
-    const int wg = warp >> 2, quarter = warp & 3;
-    const int hs = DV == 64 ? wg : 0;       // head slot of this thread's columns
-    const int h = h0 + hs;
-    const bool live = h < hend;
-    const int row = quarter * 32 + lane;    // token of M, Y and Z, key channel of D
-    const int col0 = DV == 64 ? 0 : wg * 64;
+  } else if (warp >= kFirstState) {
+    // ---------------------------------------------------------- the state
+    take_registers<kStateRegs>();
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;    // value row, lane of D
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
-    const bool owns = row < DK;             // has a key channel of the state
-    const size_t tile_off = ((ntiles > 1 ? size_t(tile) : seq) * p.H + h) * size_t(DV) * DK +
-                            size_t(col0) * DK + row;
-    float S[64];
-#pragma unroll
-    for (int i = 0; i < 64; ++i) S[i] = 0.f;
-    uint32_t pair_ph = 0;
+    const int hd = DV == 64 ? quarter >> 1 : 0;
+    const bool owns = h0 + hd < hend;
+    const int p0 = DV == 64 ? (quarter & 1) * 32 : quarter * 32;  // the warp's first row of its head
+    const size_t head_off = (seq * p.H + h0 + hd) * size_t(DV) * DK + size_t(p0) * DK;
+    const size_t tile_off = (size_t(tile) * p.H + h0 + hd) * size_t(DV) * DK + p0 + lane;
+    // The state comes and goes through D's place in TMEM: global rows are
+    // touched 32 bytes by 4 lanes, the registers hold a row a lane.
+    const size_t piece = head_off + size_t(lane >> 2) * DK + 2 * (lane & 3);
     float decay = 0.f;  // log2 of everything forgotten in this tile (STATES)
-    const float* in = STATES ? nullptr : (ntiles > 1 ? p.ws : p.S0);
-    if (in != nullptr && live && owns) {
+    float S[DK];
+    {
+      const bool ws = !STATES && owns && ntiles > 1, user = !STATES && owns && ntiles == 1 && p.S0 != nullptr;
+#pragma unroll 1
+      for (int b = 0; b < DK / 32; ++b) {
+        const uint32_t to = tmem + kColD + b * 32 + lanes;
+        float x[32];
+        if (user) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) S[i] = in[tile_off + size_t(i) * DK];
-    }
-    const float dskip = !STATES && live && p.d != nullptr ? p.d[h] : 0.f;
-    auto put_state = [&]() {
-      if (!owns) return;
+          for (int i = 0; i < 16; ++i) {
+            const float2 v = *reinterpret_cast<const float2*>(
+                p.S0 + piece + size_t((i >> 3) * 16 + (i & 1) * 8) * DK + b * 32 + ((i >> 1) & 3) * 8);
+            x[2 * i] = v.x;
+            x[2 * i + 1] = v.y;
+          }
+          tmem_st_16x32(to, *reinterpret_cast<float(*)[16]>(x));
+          tmem_st_16x32(to + (16u << 16), *reinterpret_cast<float(*)[16]>(x + 16));
+        } else {
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
-        const uint4 r = make_uint4(pack_bf(S[8 * ch], S[8 * ch + 1]), pack_bf(S[8 * ch + 2], S[8 * ch + 3]),
-                                   pack_bf(S[8 * ch + 4], S[8 * ch + 5]), pack_bf(S[8 * ch + 6], S[8 * ch + 7]));
-        *reinterpret_cast<uint4*>(sS + wg * L::kSBox + row * 128 + ((ch ^ (row & 7)) << 4)) = r;
+          for (int i = 0; i < 32; ++i) x[i] = ws ? p.ws[tile_off + size_t(b * 32 + i) * DV] : 0.f;
+          tmem_st32(to, x);
+        }
       }
+      tmem_wait_st();
+#pragma unroll
+      for (int b = 0; b < DK / 32; ++b)
+        tmem_ld32(tmem + kColD + b * 32 + lanes, *reinterpret_cast<float(*)[32]>(S + 32 * b));
+      tmem_wait_ld();
+      tc_fence_before();
+    }
+    auto put8 = [&](int i) {  // eight channels as bf16
+      *reinterpret_cast<uint4*>(sS + (i / 8) * L::kBox + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+          make_uint4(pack_bf(S[8 * i], S[8 * i + 1]), pack_bf(S[8 * i + 2], S[8 * i + 3]),
+                     pack_bf(S[8 * i + 4], S[8 * i + 5]), pack_bf(S[8 * i + 6], S[8 * i + 7]));
     };
     if (!STATES) {
-      put_state();
+#pragma unroll
+      for (int i = 0; i < DK / 8; ++i) put8(i);
       fence_async_smem();
     }
-    warp_arrive(&bars[kSReady], lane);
+    if (!STATES) warp_arrive(&bars[kSReady], lane);
+    for (int c = 0; c < nch; ++c) {
+      const uint32_t ph = uint32_t(c) & 1u;
+      const int buf = c & 1;
+      DL_WAIT_WARP(kWts0 + buf, (c >> 1) & 1);
+      const float tot = fT[buf * 2 + hd];
+      const float keep = exp2f(tot);
+      decay += tot;
+      warp_arrive(&bars[kWtsFree0 + buf], lane);
+      DL_WAIT_WARP(kD0 + ph, (c >> 1) & 1);
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < DK / 16; ++b) {
+        float x[16];
+        tmem_ld16(tmem + (STATES && ph ? kColG : kColD) + b * 16 + lanes, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[b * 16 + i] = fmaf(S[b * 16 + i], keep, x[i]);
+        if (!STATES) {  // Y, which reads the last one, was issued before D's end
+          put8(2 * b);
+          put8(2 * b + 1);
+        }
+      }
+      if (!STATES) fence_async_smem();
+      tc_fence_before();
+      warp_arrive(&bars[STATES ? kSReady + ph : kSReady], lane);
+    }
+    if (STATES) {
+      if (owns) {
+#pragma unroll
+        for (int i = 0; i < DK; ++i) p.ws[tile_off + size_t(i) * DV] = S[i];
+        if (p0 + lane == 0) p.wdecay[size_t(tile) * p.H + h0 + hd] = decay;
+      }
+    } else if (owns && last_tile && p.S1 != nullptr) {
+#pragma unroll
+      for (int b = 0; b < DK / 32; ++b)
+        tmem_st32(tmem + kColD + b * 32 + lanes, *reinterpret_cast<float(*)[32]>(S + 32 * b));
+      tmem_wait_st();
+#pragma unroll 1
+      for (int b = 0; b < DK / 32; ++b) {
+        const uint32_t from = tmem + kColD + b * 32 + lanes;
+        float x[32];
+        tmem_ld_16x32(from, *reinterpret_cast<float(*)[16]>(x));
+        tmem_ld_16x32(from + (16u << 16), *reinterpret_cast<float(*)[16]>(x + 16));
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<float2*>(p.S1 + piece + size_t((i >> 3) * 16 + (i & 1) * 8) * DK + b * 32 +
+                                     ((i >> 1) & 3) * 8) = make_float2(x[2 * i], x[2 * i + 1]);
+      }
+    }
+  } else if (!STATES) {
+    // ----------------------------------------------------------- M and o
+    take_registers<kElemRegs>();
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;    // token
+    const uint32_t lanes = uint32_t(quarter * 32) << 16;
+    // Y: 64 value columns of head slot hs
+    const int hs = DV == 64 ? wg : 0;
+    const int h = h0 + hs;
+    const bool live = h < hend;
+    const int col0 = DV == 64 ? 0 : wg * 64;
+    const float dskip = live && p.d != nullptr ? p.d[h] : 0.f;
     for (int c = 0; c < nch; ++c) {
       const uint32_t ph = uint32_t(c) & 1u;
       const int buf = c & 1;
       const int t0 = begin + c * kQ;
       const int len = min(kQ, end - t0);
       DL_WAIT_WARP(kWts0 + buf, (c >> 1) & 1);
-      const float tot = fT[buf * 2 + hs];
-      float grow = 0.f;
-      if (!STATES) {
-        const float* s = fS + (buf * 2 + hs) * kQ;
-        const float st = s[row];
-        grow = ex2(tot - st);
-        const float far = ex2(s[quarter * 32] - st);
-        const uint64_t far2 = f2_pack(far, far);
-        DL_WAIT_WARP(kG, ph);
-        tc_fence_after();
-        constexpr int kStep = DV == 64 ? 1 : 2;  // at d_v = 128 the groups take turns
-        int cb = DV == 64 ? 0 : wg;
-        float x[32];
-        tmem_ld32(tmem + kColG + cb * 32 + lanes, x);
+      const float grow = ex2(fT[buf * 2 + hs] - fS[(buf * 2 + hs) * kQ + row]);
+      float st[kHeads];
+#pragma unroll
+      for (int e = 0; e < kHeads; ++e) st[e] = fS[(buf * 2 + e) * kQ + row];
+      DL_WAIT_WARP(kG, ph);
+      tc_fence_after();
+      if (c > 0) {  // by now the last chunk's outputs have left its value stage
+        if (lane == 0) tma_store_read();
+        warp_arrive(&bars[kVFree0 + (buf ^ 1)], lane);
+      }
+      // M's blocks below the diagonal are formed by one group for both heads
+      // (at d_v = 64 the groups take turns, at 128 group 0 has them), so that
+      // they can take G's place at once.  The diagonal one has two readers at
+      // d_v = 64, each for its head, and goes in once both have read it.
+      float x[32];
+      uint32_t m[16];
+      const uint32_t at = tmem + kColG + lanes;
+      constexpr int kStep = kHeads;
+      if (kHeads == 2 || wg == 1) {
+        tmem_ld32(at + quarter * 32, x);
         tmem_wait_ld();
-        if (DV == 64) {
+        if (kHeads == 2) {
           tc_fence_before();
           warp_arrive(&bars[kPair0 + quarter], lane);
         }
+        const float4* sp = reinterpret_cast<const float4*>(fS + (buf * 2 + hs) * kQ + quarter * 32);
+        const float4* dp = reinterpret_cast<const float4*>(fDt + (buf * 2 + hs) * kQ + quarter * 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 sc = sp[i], dc = dp[i];
+          const float se[4] = {sc.x, sc.y, sc.z, sc.w}, de[4] = {dc.x, dc.y, dc.z, dc.w};
+          float r[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            r[k] = on_diagonal(x[4 * i + k] * (ex2(se[k] - st[hs]) * de[k]), dskip, 4 * i + k, lane);
+          m[2 * i] = pack_bf(r[0], r[1]);
+          m[2 * i + 1] = pack_bf(r[2], r[3]);
+        }
+        if (kHeads == 2) {
+          DL_WAIT_WARP(kPair0 + quarter, ph);
+          tc_fence_after();
+        }
+        tmem_st16(at + quarter * 32 + 16 * hs, m);
+      }
+      if (kHeads == 2 || wg == 0) {
+        float far[kHeads];
+#pragma unroll
+        for (int e = 0; e < kHeads; ++e) far[e] = ex2(fS[(buf * 2 + e) * kQ + quarter * 32] - st[e]);
+        int cb = kHeads == 2 ? wg : 0;
 #pragma unroll 1
-        for (; cb <= quarter; cb += kStep) {
-          uint32_t m[16];
-          if (cb < quarter) {
-            const ulonglong2* cf = reinterpret_cast<const ulonglong2*>(
-                fC + (buf * 2 + hs) * L::kCols + 16 * quarter * (quarter - 1) + cb * 32);
+        for (; cb < quarter; cb += kStep) {
+          tmem_ld32(at + cb * 32, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kHeads; ++e) {
+            const float4* cf = reinterpret_cast<const float4*>(
+                fC + (buf * 2 + e) * L::kCols + 16 * quarter * (quarter - 1) + cb * 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const ulonglong2 f = cf[i];
-              float a, b;
-              f2_unpack(f2_mul(f2_pack(x[4 * i], x[4 * i + 1]), f2_mul(f.x, far2)), a, b);
-              m[2 * i] = pack_bf(a, b);
-              f2_unpack(f2_mul(f2_pack(x[4 * i + 2], x[4 * i + 3]), f2_mul(f.y, far2)), a, b);
-              m[2 * i + 1] = pack_bf(a, b);
+              const float4 f = cf[i];
+              m[2 * i] = pack_bf(x[4 * i] * (f.x * far[e]), x[4 * i + 1] * (f.y * far[e]));
+              m[2 * i + 1] = pack_bf(x[4 * i + 2] * (f.z * far[e]), x[4 * i + 3] * (f.w * far[e]));
             }
-          } else {
-            const ulonglong2* sp = reinterpret_cast<const ulonglong2*>(s + cb * 32);
-            const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(fDt + (buf * 2 + hs) * kQ + cb * 32);
-            const uint64_t minus = f2_pack(-st, -st);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t sj = i & 1 ? sp[i >> 1].y : sp[i >> 1].x;
-              const uint64_t dj = i & 1 ? dp[i >> 1].y : dp[i >> 1].x;
-              float e0, e1, r0, r1;
-              f2_unpack(f2_add(sj, minus), e0, e1);
-              f2_unpack(f2_mul(f2_mul(f2_pack(ex2(e0), ex2(e1)), dj), f2_pack(x[2 * i], x[2 * i + 1])), r0, r1);
-              if (2 * i == lane) r0 += dskip;
-              if (2 * i + 1 == lane) r1 += dskip;
-              m[i] = pack_bf(2 * i <= lane ? r0 : 0.f, 2 * i + 1 <= lane ? r1 : 0.f);
-            }
-          }
-          // the next block, needed or not: a load under a condition could have its
-          // registers copied before they arrive
-          tmem_ld32(tmem + kColG + min(cb + kStep, 3) * 32 + lanes, x);
-          if (DV == 64) {  // until the other head's warp has read these columns of G too
-            DL_WAIT_WARP(kPair0 + quarter, pair_ph);
-            pair_ph ^= 1u;
-            tc_fence_after();
-          }
-          tmem_st16(tmem + kColG + cb * 32 + hs * 16 + lanes, m);
-          tmem_wait_ld();
-          if (DV == 64 && cb + kStep <= quarter) {
-            tc_fence_before();
-            warp_arrive(&bars[kPair0 + quarter], lane);
+            tmem_st16(at + cb * 32 + 16 * e, m);
           }
         }
-        {
-          uint32_t z[16];
+        if (cb == quarter) cb += kStep;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = 0u;
-          for (; cb < 4; cb += kStep) tmem_st16(tmem + kColG + cb * 32 + hs * 16 + lanes, z);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(&bars[kMReady], lane);
-      }
-      DL_WAIT_WARP(kD0 + ph, (c >> 1) & 1);
-      tc_fence_after();
-      {
-        const float keep = exp2f(tot);
-        decay += tot;
+        for (int i = 0; i < 16; ++i) m[i] = 0u;
+        for (; cb < 4; cb += kStep)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float x[32];
-          tmem_ld32(tmem + kColD + wg * 64 + b * 32 + lanes, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) S[b * 32 + i] = fmaf(S[b * 32 + i], keep, x[i]);
-        }
+          for (int e = 0; e < kHeads; ++e) tmem_st16(at + cb * 32 + 16 * e, m);
       }
-      if (!STATES) {
-        put_state();  // Y, which reads the last one, was issued before D
-        fence_async_smem();
-      }
-      tc_fence_before();
-      warp_arrive(&bars[kSReady], lane);
       warp_arrive(&bars[kWtsFree0 + buf], lane);
-      if (!STATES) {
-        DL_WAIT_WARP(kZ0 + ph, (c >> 1) & 1);
-        tc_fence_after();
-        // through the warp's 32 rows of the value stage, whose last reader Z was,
-        // so that 8 lanes write a row's 128 bytes (one row a lane kept the store
-        // path busy for 3,000 cycles a chunk)
-        unsigned char* mine = sV + (buf * 2 + wg) * L::kBox + quarter * 4096;
+      // Y as it enters the sum
+      DL_WAIT_WARP(kY, ph);
+      tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float y[32], z[32];
-          tmem_ld32(tmem + kColY + wg * 64 + b * 32 + lanes, y);
-          tmem_ld32(tmem + kColZ + wg * 64 + b * 32 + lanes, z);
-          tmem_wait_ld();
+      for (int b = 0; b < 2; ++b) {
+        tmem_ld32(tmem + kColY + wg * 64 + b * 32 + lanes, x);
+        tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf(fmaf(y[8 * i + 2 * k], grow, z[8 * i + 2 * k]),
-                             fmaf(y[8 * i + 2 * k + 1], grow, z[8 * i + 2 * k + 1]));
-            *reinterpret_cast<uint4*>(mine + lane * 128 + (((b * 4 + i) ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        __syncwarp();
-        {
-          const int r0 = lane >> 3, ch = lane & 7;
-          __nv_bfloat16* o = p.o + (long long)(t0 + quarter * 32 + r0) * p.ldo + h * DV + col0 + ch * 8;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 4 * i;
-            const uint4 w = *reinterpret_cast<const uint4*>(mine + r * 128 + ((ch ^ (r & 7)) << 4));
-            if (live && quarter * 32 + r < len) *reinterpret_cast<uint4*>(o + (long long)(4 * i) * p.ldo) = w;
-          }
-        }
-        fence_async_smem();
-        tc_fence_before();
-        warp_arrive(&bars[kYFree0 + ph], lane);
+        for (int i = 0; i < 32; ++i) x[i] *= grow;
+        tmem_st32(tmem + kColY + wg * 64 + b * 32 + lanes, x);
       }
-    }
-    if (live && owns) {
-      float* out = STATES ? p.ws : (last_tile ? p.S1 : nullptr);
-      if (out != nullptr) {
-        const size_t off = STATES ? tile_off
-                                  : (seq * p.H + h) * size_t(DV) * DK + size_t(col0) * DK + row;
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&bars[kMReady], lane);
+      DL_WAIT_WARP(kZ0 + ph, (c >> 1) & 1);
+      tc_fence_after();
+      // through the warp's 32 rows of the value stage, whose last reader M V was:
+      // whole boxes leave by TMA (a row a lane kept the store path busy for 3,000
+      // cycles a chunk)
+      unsigned char* out = sV + (buf * 2 + wg) * L::kBox + quarter * 4096;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) out[off + size_t(i) * DK] = S[i];
+      for (int b = 0; b < 2; ++b) {
+        tmem_ld32(tmem + kColY + wg * 64 + b * 32 + lanes, x);
+        tmem_wait_ld();
+        if (b == 1) {
+          tc_fence_before();
+          warp_arrive(&bars[kYFree], lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(out + lane * 128 + (((4 * b + i) ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf(x[8 * i], x[8 * i + 1]), pack_bf(x[8 * i + 2], x[8 * i + 3]),
+                         pack_bf(x[8 * i + 4], x[8 * i + 5]), pack_bf(x[8 * i + 6], x[8 * i + 7]));
       }
-      if (STATES && row == 0 && col0 == 0) p.wdecay[size_t(tile) * p.H + h] = decay;
+      fence_async_smem();
+      __syncwarp();
+      if (live && quarter * 32 + 32 <= len) {
+        if (lane == 0) tma_store_2d(&mapO, h * DV + col0, t0 + quarter * 32, out);
+      } else if (live) {  // rows behind the sequence stay as they are
+        const int r0 = lane >> 3, ch = lane & 7;
+        __nv_bfloat16* o = p.o + (long long)(t0 + quarter * 32 + r0) * p.ldo + h * DV + col0 + ch * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 4 * i;
+          if (quarter * 32 + r < len)
+            *reinterpret_cast<uint4*>(o + (long long)(4 * i) * p.ldo) =
+                *reinterpret_cast<const uint4*>(out + r * 128 + ((ch ^ (r & 7)) << 4));
+        }
+      }
     }
   }
 done:
   __syncwarp();
+  if (!STATES && warp < kElemWarps && lane == 0) tma_store_read();
 #undef DL_WAIT
 #undef DL_WAIT_WARP
   __syncthreads();
@@ -742,12 +905,13 @@ done:
 }
 
 // Turns the tiles' own states into the states they enter with, in place:
-// E_0 = S0, E_{j+1} = 2^{decay_j} E_j + own_j, one thread per four elements.
+// E_0 = S0, E_{j+1} = 2^{decay_j} E_j + own_j, one thread per four value rows
+// of a key channel (the workspace holds states as [d_k, d_v]).
 template <typename Table>
 __global__ void __launch_bounds__(256)
 dl_ssm_join_kernel(const float* S0, float* ws, const float* wdecay, const __grid_constant__ Table seqs,
-                   int seq0, int H, int tile_floats) {
-  const int per = tile_floats / 1024;  // blocks per head
+                   int seq0, int H, int dk, int dv) {
+  const int floats = dk * dv, per = floats / 1024;  // blocks per head
   const int sl = int(blockIdx.x / unsigned(H * per));
   const int rest = int(blockIdx.x % unsigned(H * per));
   const int h = rest / per;
@@ -755,10 +919,12 @@ dl_ssm_join_kernel(const float* S0, float* ws, const float* wdecay, const __grid
   const int j0 = seqs.tile0[sl], j1 = seqs.tile0[sl + 1];
   if (j1 - j0 < 2) return;
   float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (S0 != nullptr)
-    e = *reinterpret_cast<const float4*>(S0 + ((size_t(seq0) + sl) * H + h) * size_t(tile_floats) + at);
+  if (S0 != nullptr) {
+    const float* src = S0 + ((size_t(seq0) + sl) * H + h) * size_t(floats) + size_t(at % dv) * dk + at / dv;
+    e = make_float4(src[0], src[dk], src[2 * dk], src[3 * dk]);
+  }
   for (int j = j0; j < j1; ++j) {
-    float4* w = reinterpret_cast<float4*>(ws + (size_t(j) * H + h) * size_t(tile_floats) + at);
+    float4* w = reinterpret_cast<float4*>(ws + (size_t(j) * H + h) * size_t(floats) + at);
     if (j + 1 == j1) {
       *w = e;
       break;
@@ -789,13 +955,13 @@ EncodeFn encode_fn() {
   return reinterpret_cast<EncodeFn>(f);
 }
 
-// Rows of `cols` bf16, boxes of 64 columns x 128 rows, 128-byte swizzle.
-bool encode_rows(CUtensorMap* m, const void* base, long long rows, int cols, long long ld) {
+// Rows of `cols` bf16, boxes of 64 columns x `box_rows` rows, 128-byte swizzle.
+bool encode_rows(CUtensorMap* m, const void* base, long long rows, int cols, long long ld, int box_rows) {
   EncodeFn f = encode_fn();
   if (f == nullptr) return false;
   const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows > 0 ? rows : 1)};
   const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
-  const cuuint32_t box[2] = {64, kQ};
+  const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
   const cuuint32_t step[2] = {1, 1};
   return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -805,12 +971,21 @@ bool encode_rows(CUtensorMap* m, const void* base, long long rows, int cols, lon
 template <int DK, int DV, bool STATES, int NS>
 cudaError_t launch_chunk(const TcParams& p, const SeqTable<NS>& tab, int seq0, unsigned grid,
                          const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                         cudaStream_t s) {
+                         const CUtensorMap& o, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   auto kern = dl_ssm_chunk_kernel<DK, DV, STATES, SeqTable<NS>>;
+  // the roles' register shares add up against what the block starts with
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa{};
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < kStartRegs) return cudaErrorInvalidConfiguration;
   const cudaError_t e = prepare_kernel(kern, done);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, TcLayout<DK>::total, s>>>(p, tab, seq0, q, k, v);
+  kern<<<grid, kThreads, TcLayout<DK>::total, s>>>(p, tab, seq0, q, k, v, o);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -824,23 +999,23 @@ cudaError_t launch_range(const SsmParams& sp, TcParams p, int seq0, int n, const
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.ws = static_cast<float*>(ws);
   p.wdecay = p.ws + size_t(tiles) * p.H * DV * DK;
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
   const long long rows = starts[seq0 + n];
-  if (!encode_rows(&q, sp.q, rows, p.G * DK, sp.ldq) || !encode_rows(&k, sp.k, rows, p.G * DK, sp.ldk) ||
-      !encode_rows(&v, sp.v, rows, p.H * DV, sp.ldv))
+  if (!encode_rows(&q, sp.q, rows, p.G * DK, sp.ldq, kQ) || !encode_rows(&k, sp.k, rows, p.G * DK, sp.ldk, kQ) ||
+      !encode_rows(&v, sp.v, rows, p.H * DV, sp.ldv, kQ) || !encode_rows(&o, sp.o, rows, p.H * DV, sp.ldo, 32))
     return cudaErrorInvalidValue;
   if (tiles > n) {
-    cudaError_t e = launch_chunk<DK, DV, true, NS>(p, tab, seq0, unsigned(grid), q, k, v, s);
+    cudaError_t e = launch_chunk<DK, DV, true, NS>(p, tab, seq0, unsigned(grid), q, k, v, o, s);
     if (e != cudaSuccess) return e;
     const long long blocks = (long long)n * p.H * (DV * DK / 1024);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     dl_ssm_join_kernel<SeqTable<NS>><<<unsigned(blocks), 256, 0, s>>>(
-        sp.S0, p.ws, p.wdecay, tab, seq0, p.H, DV * DK);
+        sp.S0, p.ws, p.wdecay, tab, seq0, p.H, DK, DV);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  return launch_chunk<DK, DV, false, NS>(p, tab, seq0, unsigned(grid), q, k, v, s);
+  return launch_chunk<DK, DV, false, NS>(p, tab, seq0, unsigned(grid), q, k, v, o, s);
 }
 
 template <int DK, int DV>
@@ -863,10 +1038,10 @@ int cta_pairs(int H, int G, int dv) {
 }  // namespace
 
 // Tile length: one CTA runs per SM, and a cut tile costs a second walk over
-// its k and v (about kStatesCost of a full one), so take the length whose
+// its k and v (kStatesCost of a full one: 1.9 of 3.9 us a chunk), so take the length whose
 // waves of CTAs finish first.
 SsmPlan plan_ssm(int H, int G, int dk, int dv, int n, const int32_t* starts, int sms) {
-  constexpr double kStatesCost = 0.4, kTileCost = 1.0;  // in chunks
+  constexpr double kStatesCost = 0.5, kTileCost = 1.0;  // in chunks
   const int pairs = cta_pairs(H, G, dv);
   long long longest = 0;
   for (int i = 0; i < n; ++i) {
