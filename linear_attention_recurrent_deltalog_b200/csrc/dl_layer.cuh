@@ -51,17 +51,28 @@ struct SsmParams {
 };
 
 cudaError_t launch_ssm_step(const SsmParams& p, int B, int dk, int dv, bool bf16, cudaStream_t s);
-cudaError_t launch_ssm_scan(const SsmParams& p, int n, const int32_t* starts, int dk, int dv,
-                            bool bf16, cudaStream_t s);
 
 // How a prompt call is cut along its sequences, and the workspace that takes.
 struct SsmPlan {
   int tile_tokens;
   size_t bytes;
 };
+// Workspace of the largest launch of a call: where some sequence is cut, every
+// tile's state and its decay.
+size_t ssm_tile_bytes(int H, int dk, int dv, int n, const int32_t* starts, int tile_tokens);
+
+// bf16 rows, on the tensor cores.
 SsmPlan plan_ssm(int H, int G, int dk, int dv, int n, const int32_t* starts, int sms);
 cudaError_t launch_ssm_chunked(const SsmParams& p, int n, const int32_t* starts, int dk, int dv,
                                const SsmPlan& plan, void* ws, cudaStream_t s);
+// fp32 rows, or no rows at all.
+SsmPlan plan_ssm_scan(int H, int dk, int dv, int n, const int32_t* starts, int sms);
+cudaError_t launch_ssm_scan(const SsmParams& p, int n, const int32_t* starts, int dk, int dv,
+                            const SsmPlan& plan, void* ws, cudaStream_t s);
+// Own states of the tiles of sequences seq0 .. -> states they enter with.
+template <int NS>
+cudaError_t launch_ssm_join(const SsmParams& p, float* ws, const float* wdecay, const SeqTable<NS>& tab,
+                            int seq0, int n, int dk, int dv, cudaStream_t s);
 
 constexpr int kOutF32 = 0, kOutBF16 = 1, kOutE4M3 = 2;
 

@@ -123,8 +123,9 @@ int plan_sms() {
 }
 
 dl::SsmPlan ssm_plan(const dl_ssm_config& c, int32_t n, const int32_t* starts) {
-  if (c.in_dtype != DL_BF16 || n == 0) return dl::SsmPlan{};
-  return dl::plan_ssm(c.H, c.G, c.d_k, c.d_v, n, starts, plan_sms());
+  if (c.in_dtype == DL_BF16 && starts[n] > starts[0])
+    return dl::plan_ssm(c.H, c.G, c.d_k, c.d_v, n, starts, plan_sms());
+  return dl::plan_ssm_scan(c.H, c.d_k, c.d_v, n, starts, plan_sms());
 }
 
 int status(cudaError_t e) { return e == cudaSuccess ? DL_OK : DL_ERR_CUDA; }
@@ -190,7 +191,7 @@ int dl_ssm_prompt(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, co
     return status(dl::launch_ssm_chunked(p, n, starts, cfg->d_k, cfg->d_v, plan, workspace,
                                          static_cast<cudaStream_t>(stream)));
   }
-  return status(dl::launch_ssm_scan(p, n, starts, cfg->d_k, cfg->d_v, cfg->in_dtype == DL_BF16,
+  return status(dl::launch_ssm_scan(p, n, starts, cfg->d_k, cfg->d_v, plan, workspace,
                                     static_cast<cudaStream_t>(stream)));
 }
 

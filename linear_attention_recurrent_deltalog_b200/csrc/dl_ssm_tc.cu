@@ -1007,12 +1007,7 @@ cudaError_t launch_range(const SsmParams& sp, TcParams p, int seq0, int n, const
   if (tiles > n) {
     cudaError_t e = launch_chunk<DK, DV, true, NS>(p, tab, seq0, unsigned(grid), q, k, v, o, s);
     if (e != cudaSuccess) return e;
-    const long long blocks = (long long)n * p.H * (DV * DK / 1024);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    dl_ssm_join_kernel<SeqTable<NS>><<<unsigned(blocks), 256, 0, s>>>(
-        sp.S0, p.ws, p.wdecay, tab, seq0, p.H, DK, DV);
-    count_launches(1);
-    e = cudaGetLastError();
+    e = launch_ssm_join(sp, p.ws, p.wdecay, tab, seq0, n, DK, DV, s);
     if (e != cudaSuccess) return e;
   }
   return launch_chunk<DK, DV, false, NS>(p, tab, seq0, unsigned(grid), q, k, v, o, s);
@@ -1077,7 +1072,11 @@ SsmPlan plan_ssm(int H, int G, int dk, int dv, int n, const int32_t* starts, int
     }
     if (parts == 1 && even >= 4 * one) break;  // more than enough CTAs
   }
-  // workspace of the largest launch range
+  best.bytes = ssm_tile_bytes(H, dk, dv, n, starts, best.tile_tokens);
+  return best;
+}
+
+size_t ssm_tile_bytes(int H, int dk, int dv, int n, const int32_t* starts, int tile_tokens) {
   long long most = 0;
   bool any = false;
   const int step = n <= kSmallSeqs ? (n > 0 ? n : 1) : kLargeSeqs;
@@ -1086,14 +1085,27 @@ SsmPlan plan_ssm(int H, int G, int dk, int dv, int n, const int32_t* starts, int
     const int m = n - s0 < step ? n - s0 : step;
     for (int i = s0; i < s0 + m; ++i) {
       const long long len = (long long)starts[i + 1] - starts[i];
-      tiles += len > best.tile_tokens ? (len + best.tile_tokens - 1) / best.tile_tokens : 1;
+      tiles += len > tile_tokens ? (len + tile_tokens - 1) / tile_tokens : 1;
     }
     any = any || tiles > m;
     most = tiles > most ? tiles : most;
   }
-  best.bytes = any ? size_t(most) * H * (size_t(dv) * dk + 1) * 4 : 0;
-  return best;
+  return any ? size_t(most) * H * (size_t(dv) * dk + 1) * 4 : 0;
 }
+
+template <int NS>
+cudaError_t launch_ssm_join(const SsmParams& p, float* ws, const float* wdecay, const SeqTable<NS>& tab,
+                            int seq0, int n, int dk, int dv, cudaStream_t s) {
+  const long long blocks = (long long)n * p.H * (dv * dk / 1024);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  dl_ssm_join_kernel<SeqTable<NS>><<<unsigned(blocks), 256, 0, s>>>(p.S0, ws, wdecay, tab, seq0, p.H, dk, dv);
+  count_launches(1);
+  return cudaGetLastError();
+}
+template cudaError_t launch_ssm_join<kSmallSeqs>(const SsmParams&, float*, const float*, const SeqTable<kSmallSeqs>&,
+                                                 int, int, int, int, cudaStream_t);
+template cudaError_t launch_ssm_join<kLargeSeqs>(const SsmParams&, float*, const float*, const SeqTable<kLargeSeqs>&,
+                                                 int, int, int, int, cudaStream_t);
 
 cudaError_t launch_ssm_chunked(const SsmParams& sp, int n, const int32_t* starts, int dk, int dv,
                                const SsmPlan& plan, void* ws, cudaStream_t s) {
