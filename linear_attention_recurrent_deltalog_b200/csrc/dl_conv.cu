@@ -93,9 +93,16 @@ struct Taps {
   }
 };
 
-// x / (1 + e^-x): __expf and __fdividef are within a few ulp here, below the
-// rounding of either output type's tolerance; e^-x = inf gives -0.
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+// x / (1 + e^-x) with the hardware's exponential and reciprocal, each within a
+// few ulp, below the rounding of either output type's tolerance.  Their forms
+// that flush denormals need no scaling around them (half of the kernel's
+// instructions otherwise); e^-x = inf gives -0.
+__device__ __forceinline__ float silu(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return x * r;
+}
 
 // One output row from the W rows old[0 .. W-2], cur.
 template <int VEC, int W>
@@ -128,7 +135,7 @@ __device__ __forceinline__ Raw<T, VEC> state_row(const ConvParams& p, size_t s, 
   return load_raw<T, VEC>(static_cast<const T*>(p.h0) + (s * (W - 1) + r) * size_t(p.C) + c);
 }
 
-constexpr int kRowsInFlight = 8;
+constexpr int kRowsInFlight = 4;
 
 template <typename T, int VEC, int W, typename Table>
 __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 2 ? 3 : 2)
@@ -147,11 +154,17 @@ dl_conv_prompt_kernel(const ConvParams p, const __grid_constant__ Table seqs, in
   const T* x = static_cast<const T*>(p.x) + c;
   T* y = static_cast<T*>(p.y) + c;
   constexpr int U = kRowsInFlight;
-  Raw<T, VEC> cur[U];
+  Raw<T, VEC> next[U];
   auto fetch = [&](int t) {
+    const T* src = x + (long long)t * p.ldx;
+    if (t + U <= t1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < t1) cur[u] = load_raw<T, VEC>(x + (long long)(t + u) * p.ldx);
+      for (int u = 0; u < U; ++u) next[u] = load_raw<T, VEC>(src + u * p.ldx);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t + u < t1) next[u] = load_raw<T, VEC>(src + u * p.ldx);
+    }
   };
   fetch(t0);
   const Taps<VEC, W> taps(p, c);
@@ -178,14 +191,26 @@ dl_conv_prompt_kernel(const ConvParams p, const __grid_constant__ Table seqs, in
       *reinterpret_cast<Raw<T, VEC>*>(static_cast<T*>(p.h1) + (s * (W - 1) + j) * size_t(p.C) + c) = nh[j];
   }
   for (int t = t0; t < t1; t += U) {
-    if (t != t0) fetch(t);
+    Raw<T, VEC> cur[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) cur[u] = next[u];
+    fetch(t + U);
+    float o[U][VEC];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float in[VEC], o[VEC];
+      float in[VEC];
       unpack(cur[u], in);
-      taps_row<VEC, W>(taps, old, in, p.silu != 0, o);
-      if (t + u < t1) store_vec(y + (long long)(t + u) * p.ldy, o);
+      taps_row<VEC, W>(taps, old, in, p.silu != 0, o[u]);
       shift<VEC, W>(old, in);
+    }
+    T* dst = y + (long long)t * p.ldy;
+    if (t + U <= t1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) store_vec(dst + u * p.ldy, o[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t + u < t1) store_vec(dst + u * p.ldy, o[u]);
     }
   }
 }
@@ -236,12 +261,16 @@ cudaError_t conv_prompt_range(const ConvParams& p, const int32_t* starts, int s0
                               cudaStream_t s) {
   SeqTable<NS> tab;
   const int nvec = p.C / VEC;
-  // 32 rows a tile re-read 3 of 32; where that leaves the device half empty,
-  // one batch of rows in flight a tile (0.3 us less at T = 300, C = 777)
-  int tile = 4 * kRowsInFlight;
+  // Tiles that fill whole waves of threads, 96 rows at most (T = 8192, C = 4352:
+  // 80 rows and one wave 2 us less than 32 rows and two and a half), 8 at least:
+  // a tile re-reads W - 1 rows.
+  const long long rows = (long long)starts[s0 + n] - starts[s0];
+  const long long deep = (rows * nvec + one_wave() - 1) / one_wave();  // rows a thread in one wave
+  const long long waves = (deep + 95) / 96;
+  int tile = waves == 0 ? 8 : int((deep + waves * 8 - 1) / (waves * 8)) * 8;
   long long total = fill_seqs(tab, starts, s0, n, tile) * nvec;
-  if (total < one_wave() / 2) {
-    tile = kRowsInFlight;
+  for (int i = 0; i < 4 && tile > 8 && total > waves * one_wave(); ++i) {  // the sequences' last, short tiles
+    tile += 8;
     total = fill_seqs(tab, starts, s0, n, tile) * nvec;
   }
   if (total > 0xffffffffLL - kConvThreads) return cudaErrorInvalidConfiguration;

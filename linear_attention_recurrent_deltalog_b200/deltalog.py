@@ -19,6 +19,7 @@ import ctypes
 import dataclasses
 import functools
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -81,6 +82,9 @@ class dl_norm_config(ctypes.Structure):
         [("eps", ctypes.c_float)]
 
 
+_pack_ssm_io = struct.Struct("=8Q5q").pack  # dl_ssm_io's layout, quicker than the Structure
+assert struct.calcsize("=8Q5q") == ctypes.sizeof(dl_ssm_io)
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
@@ -88,7 +92,6 @@ _SZ = ctypes.POINTER(ctypes.c_size_t)
 _CFG = ctypes.POINTER(dl_config)
 _CONV = ctypes.POINTER(dl_conv_config)
 _SSM = ctypes.POINTER(dl_ssm_config)
-_SSM_IO = ctypes.POINTER(dl_ssm_io)
 _NORM = ctypes.POINTER(dl_norm_config)
 
 _SIGS = {
@@ -103,8 +106,8 @@ _SIGS = {
     "dl_conv_prompt": (_I, [_CONV, _I, _P, _P, _L, _P, _P, _P, _P, _P, _L, _P]),
     "dl_conv_step": (_I, [_CONV, _I, _P, _L, _P, _P, _P, _P, _L, _P]),
     "dl_ssm_bytes": (_I, [_SSM, _I, _P, _SZ]),
-    "dl_ssm_prompt": (_I, [_SSM, _I, _P, _SSM_IO, _P, _P, _P, ctypes.c_size_t, _P]),
-    "dl_ssm_step": (_I, [_SSM, _I, _SSM_IO, _P, _P]),
+    "dl_ssm_prompt": (_I, [_SSM, _I, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dl_ssm_step": (_I, [_SSM, _I, _P, _P, _P]),
     "dl_norm": (_I, [_NORM, _L, _P, _L, _P, _L, _P, _P, _L, _P, _L, _P, _P]),
     "dl_state_fill": (_I, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "dl_state_destroy": (_I, [_P]),
@@ -204,6 +207,10 @@ class ConvConfig:
                               DL_CONV_SILU if self.silu else 0)
 
     @functools.cached_property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+    @functools.cached_property
     def torch_in_dtype(self) -> torch.dtype:
         return _TORCH_IN[DTYPE_IDS[self.in_dtype]]
 
@@ -224,6 +231,10 @@ class SsmConfig:
     def c(self) -> dl_ssm_config:
         return dl_ssm_config(self.H, self.G, self.d_k, self.d_v, DTYPE_IDS[self.in_dtype],
                              DL_SSM_SOFTPLUS if self.softplus else 0)
+
+    @functools.cached_property
+    def ref(self):
+        return ctypes.byref(self.c)
 
     @functools.cached_property
     def torch_in_dtype(self) -> torch.dtype:
@@ -248,6 +259,10 @@ class NormConfig:
                               self.block, float(self.eps))
 
     @functools.cached_property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+    @functools.cached_property
     def torch_in_dtype(self) -> torch.dtype:
         return _TORCH_IN[DTYPE_IDS[self.in_dtype]]
 
@@ -255,7 +270,7 @@ class NormConfig:
     def torch_out_dtype(self) -> torch.dtype:
         return _TORCH_IN[OUT_DTYPE_IDS[self.out_dtype]]
 
-    @property
+    @functools.cached_property
     def scales_per_row(self) -> int:
         return -(-self.D // self.block) if self.block else 1
 
@@ -274,7 +289,7 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         if torch.cuda.is_initialized():
             # the handle alone: current_stream() would build a Stream object per call
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return None
     if isinstance(stream, int):
         return stream
@@ -289,12 +304,23 @@ def _need(t, name: str, numel: int, dtype: torch.dtype) -> None:
         if isinstance(t, int):
             return
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, need {numel}")
+
+
+def _flat(t, name: str, numel: int, dtype: torch.dtype) -> Optional[int]:
+    """The same for a tensor (or None); returns its address."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
+        _need(t, name, numel, dtype)
+    return t.data_ptr()
 
 
 def _check_step_tensors(cfg: Config, q, k, v, decay, beta, bonus, o) -> None:
@@ -320,20 +346,22 @@ def _rows(t, name: str, rows: int, cols: int, dtype: torch.dtype) -> int:
     whose rows may lie apart but are contiguous themselves."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     shape, ld = t.shape, t.stride()
     if len(shape) == 2:
-        ok = shape[1] == cols and (ld[1] == 1 or cols == 1)
+        n, width = shape
+        ok = width == cols and (ld[1] == 1 or cols == 1)
     else:
+        n = shape[0] if shape else 0
         ok = len(shape) == 3 and shape[1] * shape[2] == cols and \
-            (shape[0] == 0 or t[0].is_contiguous())
+            (n == 0 or t[0].is_contiguous())
     if not ok:
         raise ValueError(f"{name}: expected rows of {cols} contiguous elements, got shape "
                          f"{tuple(shape)} with strides {ld}")
-    if shape[0] < rows:
-        raise ValueError(f"{name}: {shape[0]} rows, need {rows}")
-    if shape[0] <= 1:
+    if n < rows:
+        raise ValueError(f"{name}: {n} rows, need {rows}")
+    if n <= 1:
         return cols  # the one row's stride is never used
     if ld[0] < cols:
         raise ValueError(f"{name}: rows overlap (stride {ld[0]}, {cols} elements)")
@@ -342,28 +370,27 @@ def _rows(t, name: str, rows: int, cols: int, dtype: torch.dtype) -> int:
 
 def _on_device(names: str, *tensors) -> None:
     """Every tensor (or None) on the current CUDA device, whose stream the call uses."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{names.split()[i]}: expected a torch.Tensor")
-        if t.get_device() != dev:
-            raise ValueError(f"{names.split()[i]}: must be on the current CUDA device, "
-                             f"not {t.device}")
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            name = names.split()[[x is t for x in tensors].index(True)]
+            raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+
+
+_INT32 = np.dtype(np.int32)
 
 
 def _starts(starts):
-    """-> (host int32 array, n, rows): sequence s holds rows starts[s] .. starts[s+1] - 1."""
+    """-> (address of a host int32 array, n, rows, the array): sequence s holds rows starts[s] ..
+    starts[s+1] - 1."""
     a = starts if isinstance(starts, np.ndarray) else np.asarray(starts)
     if a.ndim != 1 or a.size < 1 or a.dtype.kind not in "iu":
         raise ValueError("starts: expected n + 1 integers on the host")
-    if a.dtype != np.int32:
-        if a.size and (int(a.min()) < 0 or int(a.max()) > 0x7fffffff):
+    if a.dtype is not _INT32 or not a.flags.c_contiguous:
+        if int(a.min()) < 0 or int(a.max()) > 0x7fffffff:
             raise ValueError("starts: must fit int32 and be >= 0")
-        a = a.astype(np.int32)
-    a = np.ascontiguousarray(a)
-    return a, a.size - 1, int(a[-1])
+        a = np.ascontiguousarray(a, dtype=np.int32)
+    return a.__array_interface__["data"][0], a.size - 1, int(a[-1]), a
 
 
 # ----------------------------------------------------------------- C entry points
@@ -430,61 +457,68 @@ def dl_eager_step(cfg: Config, S, q, k, v, decay, beta, bonus, o, stream=None) -
                               _ptr(beta), _ptr(bonus), _ptr(o), _stream(stream)), "dl_eager_step")
 
 
-def _conv_args(cfg: ConvConfig, rows: int, n: int, x, w, bias, h0, h1, y):
-    t = cfg.torch_in_dtype
-    ldx = _rows(x, "x", rows, cfg.C, t)
-    ldy = _rows(y, "y", rows, cfg.C, t)
-    _need(w, "w", cfg.C * cfg.W, torch.float32)
-    _need(bias, "bias", cfg.C, torch.float32)
-    _need(h0, "h0", n * (cfg.W - 1) * cfg.C, t)
-    _need(h1, "h1", n * (cfg.W - 1) * cfg.C, t)
-    _on_device("x w bias h0 h1 y", x, w, bias, h0, h1, y)
-    return ldx, ldy
-
-
 def dl_conv_prompt(cfg: ConvConfig, starts, x, w, bias, h0, h1, y, stream=None) -> None:
     """y = short causal convolution of packed sequences; ``h0`` (or None) and
     ``h1`` (or None, or ``h0``) are the states [n, W-1, C] before and after."""
-    a, n, rows = _starts(starts)
-    ldx, ldy = _conv_args(cfg, rows, n, x, w, bias, h0, h1, y)
-    _check(_lib.dl_conv_prompt(ctypes.byref(cfg.c), n, a.ctypes.data, x.data_ptr(), ldx,
-                               w.data_ptr(), _ptr(bias), _ptr(h0), _ptr(h1), y.data_ptr(), ldy,
-                               _stream(stream)), "dl_conv_prompt")
+    at, n, rows, keep = _starts(starts)
+    C, W, t = cfg.C, cfg.W, cfg.torch_in_dtype
+    ldx = _rows(x, "x", rows, C, t)
+    ldy = _rows(y, "y", rows, C, t)
+    if w is None:
+        raise TypeError("w: expected a torch.Tensor")
+    pw = _flat(w, "w", C * W, torch.float32)
+    pb = _flat(bias, "bias", C, torch.float32)
+    ph0 = _flat(h0, "h0", n * (W - 1) * C, t)
+    ph1 = _flat(h1, "h1", n * (W - 1) * C, t)
+    _on_device("x w bias h0 h1 y", x, w, bias, h0, h1, y)
+    rc = _lib.dl_conv_prompt(cfg.ref, n, at, x.data_ptr(), ldx, pw, pb, ph0, ph1,
+                             y.data_ptr(), ldy, _stream(stream))
+    if rc:
+        _check(rc, "dl_conv_prompt")
 
 
 def dl_conv_step(cfg: ConvConfig, x, w, bias, h, y, stream=None) -> None:
     """One token of each of x.shape[0] sequences; the state ``h`` is updated in place."""
     B = x.shape[0]
-    ldx, ldy = _conv_args(cfg, B, B, x, w, bias, h, None, y)
-    if h is None:
-        raise TypeError("h: expected a torch.Tensor")
-    _check(_lib.dl_conv_step(ctypes.byref(cfg.c), B, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias),
-                             h.data_ptr(), y.data_ptr(), ldy, _stream(stream)), "dl_conv_step")
+    C, W, t = cfg.C, cfg.W, cfg.torch_in_dtype
+    ldx = _rows(x, "x", B, C, t)
+    ldy = _rows(y, "y", B, C, t)
+    if w is None or h is None:
+        raise TypeError("w, h: expected a torch.Tensor")
+    pw = _flat(w, "w", C * W, torch.float32)
+    pb = _flat(bias, "bias", C, torch.float32)
+    ph = _flat(h, "h", B * (W - 1) * C, t)
+    _on_device("x w bias h y", x, w, bias, h, y)
+    rc = _lib.dl_conv_step(cfg.ref, B, x.data_ptr(), ldx, pw, pb, ph, y.data_ptr(), ldy,
+                           _stream(stream))
+    if rc:
+        _check(rc, "dl_conv_step")
 
 
 def dl_ssm_bytes(cfg: SsmConfig, starts) -> int:
     """Bytes of workspace ``dl_ssm_prompt`` needs for these lengths."""
-    a, n, _ = _starts(starts)
+    at, n, _, keep = _starts(starts)
     b = ctypes.c_size_t()
-    _check(_lib.dl_ssm_bytes(ctypes.byref(cfg.c), n, a.ctypes.data, ctypes.byref(b)),
+    _check(_lib.dl_ssm_bytes(cfg.ref, n, at, ctypes.byref(b)),
            "dl_ssm_bytes")
     return b.value
 
 
 def _ssm_io(cfg: SsmConfig, rows: int, n: int, q, k, v, dt, a, d, dt_bias, o, S0, S1):
-    t, H = cfg.torch_in_dtype, cfg.H
+    """-> (dl_ssm_io as bytes, addresses of S0 and S1)"""
+    t, H, f32 = cfg.torch_in_dtype, cfg.H, torch.float32
     nk, nv = cfg.G * cfg.d_k, H * cfg.d_v
-    ld = (_rows(q, "q", rows, nk, t), _rows(k, "k", rows, nk, t), _rows(v, "v", rows, nv, t),
-          _rows(dt, "dt", rows, H, torch.float32), _rows(o, "o", rows, nv, t))
+    ldq, ldk = _rows(q, "q", rows, nk, t), _rows(k, "k", rows, nk, t)
+    ldv, ldo = _rows(v, "v", rows, nv, t), _rows(o, "o", rows, nv, t)
+    lddt = _rows(dt, "dt", rows, H, f32)
     if a is None:
         raise TypeError("a: expected a torch.Tensor")
-    for name, x in (("a", a), ("d", d), ("dt_bias", dt_bias)):
-        _need(x, name, H, torch.float32)
-    _need(S0, "S0", n * nv * cfg.d_k, torch.float32)
-    _need(S1, "S1", n * nv * cfg.d_k, torch.float32)
+    pa, pd, pb = _flat(a, "a", H, f32), _flat(d, "d", H, f32), _flat(dt_bias, "dt_bias", H, f32)
+    p0 = _flat(S0, "S0", n * nv * cfg.d_k, f32)
+    p1 = _flat(S1, "S1", n * nv * cfg.d_k, f32)
     _on_device("q k v dt a d dt_bias o S0 S1", q, k, v, dt, a, d, dt_bias, o, S0, S1)
-    return dl_ssm_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), a.data_ptr(),
-                     _ptr(d), _ptr(dt_bias), o.data_ptr(), *ld)
+    return _pack_ssm_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), pa, pd or 0,
+                        pb or 0, o.data_ptr(), ldq, ldk, ldv, lddt, ldo), p0, p1
 
 
 def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o, workspace=None,
@@ -493,48 +527,57 @@ def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o,
     ``S1`` (or None, or ``S0``) are the states [n, H, d_v, d_k] before and
     after.  ``workspace``: a uint8 tensor of ``dl_ssm_bytes`` (allocated for
     the call when None)."""
-    arr, n, rows = _starts(starts)
-    io = _ssm_io(cfg, rows, n, q, k, v, dt, a, d, dt_bias, o, S0, S1)
+    at, n, rows, keep = _starts(starts)
+    io, p0, p1 = _ssm_io(cfg, rows, n, q, k, v, dt, a, d, dt_bias, o, S0, S1)
     if workspace is None:
-        workspace = torch.empty(dl_ssm_bytes(cfg, arr), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(dl_ssm_bytes(cfg, keep), dtype=torch.uint8, device=q.device)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
     nb = workspace.numel() * workspace.element_size()
     if not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     _on_device("workspace", workspace)
-    _check(_lib.dl_ssm_prompt(ctypes.byref(cfg.c), n, arr.ctypes.data, ctypes.byref(io), _ptr(S0),
-                              _ptr(S1), workspace.data_ptr() if nb else None, nb,
-                              _stream(stream)), "dl_ssm_prompt")
+    rc = _lib.dl_ssm_prompt(cfg.ref, n, at, io, p0, p1,
+                            workspace.data_ptr() if nb else None, nb, _stream(stream))
+    if rc:
+        _check(rc, "dl_ssm_prompt")
 
 
 def dl_ssm_step(cfg: SsmConfig, q, k, v, dt, a, d, dt_bias, S, o, stream=None) -> None:
     """One token of each of q.shape[0] sequences; the state ``S`` [B, H, d_v,
     d_k] is updated in place."""
     B = q.shape[0]
-    io = _ssm_io(cfg, B, B, q, k, v, dt, a, d, dt_bias, o, S, None)
     if S is None:
         raise TypeError("S: expected a torch.Tensor")
-    _check(_lib.dl_ssm_step(ctypes.byref(cfg.c), B, ctypes.byref(io), S.data_ptr(),
-                            _stream(stream)), "dl_ssm_step")
+    io, p, _ = _ssm_io(cfg, B, B, q, k, v, dt, a, d, dt_bias, o, S, None)
+    rc = _lib.dl_ssm_step(cfg.ref, B, io, p, _stream(stream))
+    if rc:
+        _check(rc, "dl_ssm_step")
 
 
 def dl_norm(cfg: NormConfig, x, w, out, res=None, res_out=None, scales=None, stream=None) -> None:
     """out = RMS norm of x (+ res), times w; ``res_out`` takes x + res.  An
     "e4m3" output needs ``scales`` [rows, cfg.scales_per_row]."""
-    rows, t = x.shape[0], cfg.torch_in_dtype
-    ldx = _rows(x, "x", rows, cfg.D, t)
-    ldo = _rows(out, "out", rows, cfg.D, cfg.torch_out_dtype)
-    ldr = _rows(res, "res", rows, cfg.D, t) if res is not None else cfg.D
-    ldro = _rows(res_out, "res_out", rows, cfg.D, t) if res_out is not None else cfg.D
+    rows, D, t = x.shape[0], cfg.D, cfg.torch_in_dtype
+    ldx = _rows(x, "x", rows, D, t)
+    ldo = _rows(out, "out", rows, D, cfg.torch_out_dtype)
+    ldr = ldro = D
+    pr = pro = None
+    if res is not None:
+        ldr, pr = _rows(res, "res", rows, D, t), res.data_ptr()
+    if res_out is not None:
+        ldro, pro = _rows(res_out, "res_out", rows, D, t), res_out.data_ptr()
     if w is None:
         raise TypeError("w: expected a torch.Tensor")
-    _need(w, "w", cfg.D, torch.float32)
-    if cfg.out_dtype == "e4m3" and scales is None:
+    pw = _flat(w, "w", D, torch.float32)
+    if scales is None and cfg.out_dtype == "e4m3":
         raise TypeError("scales: expected a torch.Tensor for an e4m3 output")
-    _need(scales, "scales", rows * cfg.scales_per_row, torch.float32)
+    ps = _flat(scales, "scales", rows * cfg.scales_per_row, torch.float32)
     _on_device("x w out res res_out scales", x, w, out, res, res_out, scales)
-    _check(_lib.dl_norm(ctypes.byref(cfg.c), rows, x.data_ptr(), ldx, _ptr(res), ldr, w.data_ptr(),
-                        _ptr(res_out), ldro, out.data_ptr(), ldo, _ptr(scales), _stream(stream)),
-           "dl_norm")
+    rc = _lib.dl_norm(cfg.ref, rows, x.data_ptr(), ldx, pr, ldr, pw, pro, ldro, out.data_ptr(), ldo,
+                      ps, _stream(stream))
+    if rc:
+        _check(rc, "dl_norm")
 
 
 def dl_state_fill(handle: int, cfg: Config):
