@@ -141,6 +141,11 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
 // A box of 32 rows on its way out, and the wait until its shared memory has been read.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
@@ -373,6 +378,23 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
   const int hend = (g + 1) * hpg;
   const size_t seq = size_t(seq0) + size_t(sl);
 
+  // What the roles ask for first is on its way while they are set up: the
+  // state (heads of a CTA lie side by side, here as in the workspace), dt's rows
+  // and the tensor maps.
+  {
+    const float* in = STATES ? nullptr : (ntiles > 1 ? p.ws + (size_t(tile) * p.H + h0) * size_t(DV) * DK
+                              : p.S0 != nullptr ? p.S0 + (seq * p.H + h0) * size_t(DV) * DK : nullptr);
+    const int heads = min(kHeads, hend - h0);
+    if (in != nullptr)
+      for (int i = tid; i < heads * (DV * DK / 32); i += kThreads) prefetch_l2(in + size_t(i) * 32);
+    if (tid < kQ && begin + tid < end) prefetch_l2(p.dt + (long long)(begin + tid) * p.lddt + h0);
+    if (tid == kThreads - 1) {
+      prefetch_map(&mapQ);
+      prefetch_map(&mapK);
+      prefetch_map(&mapV);
+      prefetch_map(&mapO);
+    }
+  }
   if (warp == 0) tmem_alloc(tmem_slot, 512);
   if (tid == 32) {
     for (int i = 0; i < kBars; ++i) {
@@ -654,25 +676,31 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     float S[DK];
     {
       const bool ws = !STATES && owns && ntiles > 1, user = !STATES && owns && ntiles == 1 && p.S0 != nullptr;
-#pragma unroll 1
-      for (int b = 0; b < DK / 32; ++b) {
-        const uint32_t to = tmem + kColD + b * 32 + lanes;
-        float x[32];
-        if (user) {
+      // all loads before the first store: one latency, not DK / 32
+      float x[DK / 32][32];
+      const uint32_t to = tmem + kColD + lanes;
+      if (user) {
+#pragma unroll
+        for (int b = 0; b < DK / 32; ++b)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 v = *reinterpret_cast<const float2*>(
                 p.S0 + piece + size_t((i >> 3) * 16 + (i & 1) * 8) * DK + b * 32 + ((i >> 1) & 3) * 8);
-            x[2 * i] = v.x;
-            x[2 * i + 1] = v.y;
+            x[b][2 * i] = v.x;
+            x[b][2 * i + 1] = v.y;
           }
-          tmem_st_16x32(to, *reinterpret_cast<float(*)[16]>(x));
-          tmem_st_16x32(to + (16u << 16), *reinterpret_cast<float(*)[16]>(x + 16));
-        } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = ws ? p.ws[tile_off + size_t(b * 32 + i) * DV] : 0.f;
-          tmem_st32(to, x);
+        for (int b = 0; b < DK / 32; ++b) {
+          tmem_st_16x32(to + b * 32, *reinterpret_cast<float(*)[16]>(x[b]));
+          tmem_st_16x32(to + b * 32 + (16u << 16), *reinterpret_cast<float(*)[16]>(x[b] + 16));
         }
+      } else {
+#pragma unroll
+        for (int b = 0; b < DK / 32; ++b)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[b][i] = ws ? p.ws[tile_off + size_t(b * 32 + i) * DV] : 0.f;
+#pragma unroll
+        for (int b = 0; b < DK / 32; ++b) tmem_st32(to + b * 32, x[b]);
       }
       tmem_wait_st();
 #pragma unroll
@@ -729,18 +757,20 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
       for (int b = 0; b < DK / 32; ++b)
         tmem_st32(tmem + kColD + b * 32 + lanes, *reinterpret_cast<float(*)[32]>(S + 32 * b));
       tmem_wait_st();
-#pragma unroll 1
+      float x[DK / 32][32];
+      const uint32_t from = tmem + kColD + lanes;
+#pragma unroll
       for (int b = 0; b < DK / 32; ++b) {
-        const uint32_t from = tmem + kColD + b * 32 + lanes;
-        float x[32];
-        tmem_ld_16x32(from, *reinterpret_cast<float(*)[16]>(x));
-        tmem_ld_16x32(from + (16u << 16), *reinterpret_cast<float(*)[16]>(x + 16));
-        tmem_wait_ld();
+        tmem_ld_16x32(from + b * 32, *reinterpret_cast<float(*)[16]>(x[b]));
+        tmem_ld_16x32(from + b * 32 + (16u << 16), *reinterpret_cast<float(*)[16]>(x[b] + 16));
+      }
+      tmem_wait_ld();
+#pragma unroll
+      for (int b = 0; b < DK / 32; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           *reinterpret_cast<float2*>(p.S1 + piece + size_t((i >> 3) * 16 + (i & 1) * 8) * DK + b * 32 +
-                                     ((i >> 1) & 3) * 8) = make_float2(x[2 * i], x[2 * i + 1]);
-      }
+                                     ((i >> 1) & 3) * 8) = make_float2(x[b][2 * i], x[b][2 * i + 1]);
     }
   } else if (!STATES) {
     // ----------------------------------------------------------- M and o
