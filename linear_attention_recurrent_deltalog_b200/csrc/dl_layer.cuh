@@ -70,9 +70,9 @@ SsmPlan plan_ssm_scan(int H, int dk, int dv, int n, const int32_t* starts, int s
 cudaError_t launch_ssm_scan(const SsmParams& p, int n, const int32_t* starts, int dk, int dv,
                             const SsmPlan& plan, void* ws, cudaStream_t s);
 // Own states of the tiles of sequences seq0 .. -> states they enter with.
-template <int NS>
-cudaError_t launch_ssm_join(const SsmParams& p, float* ws, const float* wdecay, const SeqTable<NS>& tab,
-                            int seq0, int n, int dk, int dv, cudaStream_t s);
+template <typename Table>
+cudaError_t launch_ssm_join(const SsmParams& p, float* ws, const float* wdecay, const Table& tab, int seq0,
+                            int n, int dk, int dv, cudaStream_t s);
 
 constexpr int kOutF32 = 0, kOutBF16 = 1, kOutE4M3 = 2;
 

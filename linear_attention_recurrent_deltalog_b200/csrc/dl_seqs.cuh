@@ -17,6 +17,7 @@ struct SeqTable {
   int start[N + 1];
   int tile0[N + 1];
 
+  __device__ __forceinline__ int index(int sl) const { return sl; }  // of a sequence in the call
   __device__ __forceinline__ int find(int tile) const {
     int lo = 0, hi = n - 1;
     while (lo < hi) {

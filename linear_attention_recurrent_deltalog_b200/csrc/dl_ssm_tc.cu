@@ -40,6 +40,8 @@
 // other, a chunk took half as long again.)
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "dl_layer.cuh"
 #include "dl_tmem.cuh"
 
@@ -94,6 +96,45 @@ enum Bar {
 };
 static_assert(kBars <= 40, "barrier slots");
 
+// The sequences of a launch, longest first, and the tiles they are cut into.
+template <int N>
+struct OrderedSeqs {
+  int n;
+  int seq[N], begin[N], end[N];  // place in the call, tokens
+  int tile0[N + 1];
+  __device__ __forceinline__ int index(int sl) const { return seq[sl]; }
+  __device__ __forceinline__ int find(int tile) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tile0[mid] <= tile)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+template <int N>
+long long fill_ordered(OrderedSeqs<N>& t, const int32_t* starts, int s0, int n, int tile) {
+  t.n = n;
+  for (int i = 0; i < n; ++i) t.seq[i] = i;
+  std::stable_sort(t.seq, t.seq + n, [&](int a, int b) {
+    return starts[s0 + a + 1] - starts[s0 + a] > starts[s0 + b + 1] - starts[s0 + b];
+  });
+  long long tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    t.begin[i] = starts[s0 + t.seq[i]];
+    t.end[i] = starts[s0 + t.seq[i] + 1];
+    t.tile0[i] = int(tiles);
+    const long long len = (long long)t.end[i] - t.begin[i];
+    tiles += len > tile ? (len + tile - 1) / tile : 1;
+  }
+  t.tile0[n] = int(tiles);
+  return tiles;
+}
+
 struct TcParams {
   const float* dt;
   const float* a;
@@ -107,8 +148,9 @@ struct TcParams {
   int* err;
   long long lddt, ldo;
   int H, G, softplus;
-  int pairs;        // CTAs per tile
+  int pairs;        // work items per tile
   int tile_tokens;
+  unsigned items;   // tiles * pairs
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -361,33 +403,54 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the warp's: uniform registers
-  const int tile = int(blockIdx.x / unsigned(p.pairs));
-  const int pair = int(blockIdx.x % unsigned(p.pairs));
-  const int sl = seqs.find(tile);
-  const int first_tile = seqs.tile0[sl], ntiles = seqs.tile0[sl + 1] - first_tile;
-  const int seq_end = seqs.start[sl + 1];
-  const int begin = seqs.start[sl] + (tile - first_tile) * p.tile_tokens;
-  const int end = min(begin + p.tile_tokens, seq_end);
-  const bool last_tile = tile - first_tile == ntiles - 1;
-  if (STATES && last_tile) return;  // nobody enters from a last tile's own state
-  const int nch = (end - begin + kQ - 1) / kQ;
-  // heads: pairs run through the heads of a group
-  const int hpg = p.H / p.G, ppg = (hpg + kHeads - 1) / kHeads;
-  const int g = pair / ppg;
-  const int h0 = g * hpg + (pair % ppg) * kHeads;
-  const int hend = (g + 1) * hpg;
-  const size_t seq = size_t(seq0) + size_t(sl);
+  // Work item: a tile of a sequence and the heads of 128 value columns.
+  struct Work {
+    int tile, begin, end, nch;
+    int g, h0, hend;
+    bool cut, last;  // the sequence has several tiles; this is its last
+    size_t seq;
+  };
+  auto work = [&](unsigned item) {
+    Work w;
+    w.tile = int(item / unsigned(p.pairs));
+    const int pair = int(item % unsigned(p.pairs));
+    const int sl = seqs.find(w.tile);
+    const int first = seqs.tile0[sl], ntiles = seqs.tile0[sl + 1] - first;
+    w.begin = seqs.begin[sl] + (w.tile - first) * p.tile_tokens;
+    w.end = min(w.begin + p.tile_tokens, seqs.end[sl]);
+    w.nch = (w.end - w.begin + kQ - 1) / kQ;
+    w.cut = ntiles > 1;
+    w.last = w.tile - first == ntiles - 1;
+    // pairs run through the heads of a group
+    const int hpg = p.H / p.G, ppg = (hpg + kHeads - 1) / kHeads;
+    w.g = pair / ppg;
+    w.h0 = w.g * hpg + (pair % ppg) * kHeads;
+    w.hend = (w.g + 1) * hpg;
+    w.seq = size_t(seq0) + size_t(seqs.index(sl));
+    return w;
+  };
+  // A CTA's items, every role's alike: items come longest first and every other
+  // round of them is dealt in reverse, so that the CTAs' shares are even.  (In
+  // STATES nobody needs a last tile.)
+#define DL_ITEMS(w)                                                                              \
+  for (unsigned round = 0, item = blockIdx.x; item < p.items;                                    \
+       ++round, item = round * gridDim.x + ((round & 1u) ? gridDim.x - 1 - blockIdx.x : blockIdx.x)) \
+    if (const Work w = work(item); !(STATES && w.last))
 
-  // What the roles ask for first is on its way while they are set up: the
-  // state (heads of a CTA lie side by side, here as in the workspace), dt's rows
-  // and the tensor maps.
+  // The state an item enters with, in the call or in the workspace; heads of an
+  // item lie side by side in both.
+  auto prefetch_state = [&](const Work& w, int at, int step) {
+    const float* in = STATES ? nullptr : (w.cut ? p.ws + (size_t(w.tile) * p.H + w.h0) * size_t(DV) * DK
+                              : p.S0 != nullptr ? p.S0 + (w.seq * p.H + w.h0) * size_t(DV) * DK : nullptr);
+    if (in == nullptr) return;
+    const int lines = min(kHeads, w.hend - w.h0) * (DV * DK / 32);
+    for (int i = at; i < lines; i += step) prefetch_l2(in + size_t(i) * 32);
+  };
+  // what the roles ask for first is on its way while they are set up
   {
-    const float* in = STATES ? nullptr : (ntiles > 1 ? p.ws + (size_t(tile) * p.H + h0) * size_t(DV) * DK
-                              : p.S0 != nullptr ? p.S0 + (seq * p.H + h0) * size_t(DV) * DK : nullptr);
-    const int heads = min(kHeads, hend - h0);
-    if (in != nullptr)
-      for (int i = tid; i < heads * (DV * DK / 32); i += kThreads) prefetch_l2(in + size_t(i) * 32);
-    if (tid < kQ && begin + tid < end) prefetch_l2(p.dt + (long long)(begin + tid) * p.lddt + h0);
+    const Work w = work(blockIdx.x);
+    prefetch_state(w, tid, kThreads);
+    if (tid < kQ && w.begin + tid < w.end) prefetch_l2(p.dt + (long long)(w.begin + tid) * p.lddt + w.h0);
     if (tid == kThreads - 1) {
       prefetch_map(&mapQ);
       prefetch_map(&mapK);
@@ -414,7 +477,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const int errh = int(seq) * p.H + h0;
+  const int errh = int(blockIdx.x);
 // One thread's wait, and a whole warp's (which gives up as one).
 #define DL_WAIT(bar, parity)                            \
   if (!wait_phase(&bars[bar], (parity), p.err, errh)) { \
@@ -432,32 +495,28 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     if (warp == kFirstCtrl) {
       // ----------------------------------------------------------- copies
       if (lane == 0) {
-        auto copy = [&](unsigned char* dst, const CUtensorMap* map, uint32_t boxes, int x, int c, int bar) {
+        auto copy = [&](unsigned char* dst, const CUtensorMap* map, uint32_t boxes, int x, int t, int bar) {
           mbar_arrive_expect_tx(&bars[bar], boxes * L::kBox);
           for (uint32_t b = 0; b < boxes; ++b)
-            tma_load_2d(dst + b * L::kBox, map, x + int(b) * 64, begin + c * kQ, &bars[bar]);
+            tma_load_2d(dst + b * L::kBox, map, x + int(b) * 64, t, &bars[bar]);
         };
-        auto copy_q = [&](int c) { copy(sQ, &mapQ, L::kKBlocks, g * DK, c, kFullQ); };
-        auto copy_k = [&](int c) { copy(sK + (c & 1) * L::kK, &mapK, L::kKBlocks, g * DK, c, kFullK0 + (c & 1)); };
-        auto copy_v = [&](int c) { copy(sV + (c & 1) * 2 * L::kBox, &mapV, 2, h0 * DV, c, kFullV0 + (c & 1)); };
-        if (!STATES && nch > 0) copy_q(0);
-        for (int c = 0; c < 2 && c < nch; ++c) {
-          copy_k(c);
-          copy_v(c);
-        }
-        // in the order in which a chunk sets buffers free: the values' (an output's
-        // on its way out, or w o V's source) and q at once, k for the next but one
-        for (int c = 0; c + 1 < nch; ++c) {
-          if (c > 0) {
-            if (!STATES) DL_WAIT(kVFree0 + ((c - 1) & 1), ((c - 1) >> 1) & 1);
-            copy_v(c + 1);
+        unsigned n = 0;
+        DL_ITEMS(w) {
+          for (int c = 0; c < w.nch; ++c, ++n) {
+            const uint32_t ph = n & 1u;
+            const int t = w.begin + c * kQ;
+            // in the order in which the buffers come free: k's last reader is D of
+            // the last chunk but one, the values' its outputs on their way out, q's
+            // the last chunk's Y
+            if (n > 1) DL_WAIT(kD0 + ph, ((n >> 1) - 1) & 1);
+            copy(sK + ph * L::kK, &mapK, L::kKBlocks, w.g * DK, t, kFullK0 + ph);
+            if (!STATES && n > 1) DL_WAIT(kVFree0 + ph, ((n >> 1) - 1) & 1);
+            copy(sV + ph * 2 * L::kBox, &mapV, 2, w.h0 * DV, t, kFullV0 + ph);
+            if (!STATES) {
+              if (n > 0) DL_WAIT(kY, (n - 1) & 1);
+              copy(sQ, &mapQ, L::kKBlocks, w.g * DK, t, kFullQ);
+            }
           }
-          if (!STATES) {
-            DL_WAIT(kY, c & 1);
-            copy_q(c + 1);
-          }
-          DL_WAIT(kD0 + (c & 1), (c >> 1) & 1);
-          if (c + 2 < nch) copy_k(c + 2);
         }
       }
     } else if (warp == kFirstCtrl + 1) {
@@ -468,14 +527,16 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
         constexpr uint32_t idY = idG;
         constexpr uint32_t idM = idesc_bf16(128, DV == 64 ? 64 : 128, false, true);
         constexpr uint32_t idD = idesc_bf16(128, DK, false, true);
-        for (int c = 0; c < nch; ++c) {
-          const uint32_t ph = uint32_t(c) & 1u;
+        unsigned n = 0;
+        DL_ITEMS(w)
+        for (int c = 0; c < w.nch; ++c, ++n) {
+          const uint32_t ph = n & 1u;
           const unsigned char* k = sK + ph * L::kK;
           const unsigned char* v = sV + ph * 2 * L::kBox;
-          DL_WAIT_WARP(kFullK0 + ph, (c >> 1) & 1);
+          DL_WAIT_WARP(kFullK0 + ph, (n >> 1) & 1);
           if (!STATES) {
             DL_WAIT_WARP(kFullQ, ph);
-            if (c > 0) DL_WAIT_WARP(kZ0 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // M, where G goes, is still being read
+            if (n > 0) DL_WAIT_WARP(kZ0 + (ph ^ 1u), ((n - 1) >> 1) & 1);  // M, where G goes, is still being read
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks)
@@ -484,15 +545,15 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
             umma_done(lead, &bars[kG]);
           }
           // STATES alternates between two accumulators (no G takes the other's
-          // place): chunk c waits for the state to have taken up c - 2
+          // place): a chunk waits for the state to have taken up the last but one
           if (!STATES) DL_WAIT_WARP(kSReady, ph);
-          if (STATES && c > 1) DL_WAIT_WARP(kSReady + ph, ((c >> 1) - 1) & 1);
+          if (STATES && n > 1) DL_WAIT_WARP(kSReady + ph, ((n >> 1) - 1) & 1);
           tc_fence_after();
           const uint32_t dcol = tmem + (STATES && ph ? kColG : kColD);
 #pragma unroll 1
           for (int pc = 0; pc < kPieces; ++pc) {
             if (!STATES && pc == kPieces / 2) {  // by now the last chunk's Y has been read
-              if (c > 0) DL_WAIT_WARP(kYFree, (c - 1) & 1);
+              if (n > 0) DL_WAIT_WARP(kYFree, (n - 1) & 1);
               tc_fence_after();
 #pragma unroll
               for (int ks = 0; ks < DK / 16; ++ks)
@@ -501,7 +562,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
               umma_done(lead, &bars[kY]);
             }
             const int st = pc % kStages;
-            DL_WAIT_WARP(kWFull0 + st, (c * (kPieces / kStages) + pc / kStages) & 1);
+            DL_WAIT_WARP(kWFull0 + st, (n * (kPieces / kStages) + pc / kStages) & 1);
             tc_fence_after();
             const uint64_t kd = desc_sw128(k + pc * (kPiece * 128), L::kBox);
 #pragma unroll
@@ -526,22 +587,25 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     } else {
       // ----------------------------------------------------------- decays
       const int hs = warp - kFirstCtrl - 2;
-      const int h = h0 + hs;
       if (hs < kHeads) {
-        const bool live = h < hend;
+        unsigned n = 0;
+        DL_ITEMS(w) {
+        const int h = w.h0 + hs;
+        const bool live = h < w.hend;
         const float a2 = live ? p.a[h] * kLog2e : 0.f;
         const float bias = live && p.bias != nullptr ? p.bias[h] : 0.f;
         float next[4];  // raw steps of the next chunk (the last row again behind the end)
         auto fetch = [&](int c) {
-          if (!live || c >= nch) return;
+          if (!live || c >= w.nch) return;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            next[e] = p.dt[(long long)min(begin + c * kQ + lane * 4 + e, end - 1) * p.lddt + h];
+            next[e] = p.dt[(long long)min(w.begin + c * kQ + lane * 4 + e, w.end - 1) * p.lddt + h];
         };
         fetch(0);
-        for (int c = 0; c < nch; ++c) {
-          const int buf = c & 1;
-          const int t0 = begin + c * kQ + lane * 4;
+        if (round > 0) prefetch_state(w, hs * 32 + lane, kHeads * 32);
+        for (int c = 0; c < w.nch; ++c, ++n) {
+          const int buf = int(n & 1u);
+          const int t0 = w.begin + c * kQ + lane * 4;
           float dt[4], lam[4], raw[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) raw[e] = next[e] + bias;
@@ -549,7 +613,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             dt[e] = p.softplus ? softplusf(raw[e]) : raw[e];
-            if (!live || t0 + e >= end) dt[e] = 0.f;
+            if (!live || t0 + e >= w.end) dt[e] = 0.f;
             lam[e] = fmaxf(dt[e] * a2, kMinLambda);
           }
           // sums over the tokens behind each one
@@ -567,7 +631,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
           s[2] = s[3] + lam[3];
           s[1] = s[2] + lam[2];
           s[0] = s[1] + lam[1];
-          if (c >= 2) DL_WAIT_WARP(kWtsFree0 + buf, ((c >> 1) - 1) & 1);
+          if (n > 1) DL_WAIT_WARP(kWtsFree0 + buf, ((n >> 1) - 1) & 1);
           const int at = (buf * 2 + hs) * kQ + lane * 4;
           *reinterpret_cast<float4*>(fS + at) = make_float4(s[0], s[1], s[2], s[3]);
           *reinterpret_cast<float4*>(fDt + at) = make_float4(dt[0], dt[1], dt[2], dt[3]);
@@ -589,6 +653,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
           if (lane == 0) fT[buf * 2 + hs] = s[0] + lam[0];
           warp_arrive(&bars[kWts0 + buf], lane);
         }
+        }
       }
     }
   } else if (warp >= kFirstWeigh) {
@@ -604,17 +669,19 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       at[i] = (quarter >> 1) * L::kBox + trow * 128 + ((((quarter & 1) * 4 + i * 2 + pblk) ^ r) << 4);
-    for (int c = 0; c < nch; ++c) {
-      const int buf = c & 1;
-      const int len = min(kQ, end - (begin + c * kQ));
+    unsigned n = 0;
+    DL_ITEMS(wk)
+    for (int c = 0; c < wk.nch; ++c, ++n) {
+      const int buf = int(n & 1u);
+      const int len = min(kQ, wk.end - (wk.begin + c * kQ));
       unsigned char* v = sV + buf * 2 * L::kBox;
       const float2* w = reinterpret_cast<const float2*>(fW + (buf * 2 + head) * kQ) + (lane & 3);
-      DL_WAIT_WARP(kWts0 + buf, (c >> 1) & 1);
-      DL_WAIT_WARP(kFullV0 + buf, (c >> 1) & 1);
+      DL_WAIT_WARP(kWts0 + buf, (n >> 1) & 1);
+      DL_WAIT_WARP(kFullV0 + buf, (n >> 1) & 1);
       if (len < kQ && odd == 0) {
         // rows behind the sequence may hold anything: zeros for the sums over
         // tokens (G's columns there are masked), in place before the first piece
-        DL_WAIT_WARP(kFullK0 + buf, (c >> 1) & 1);
+        DL_WAIT_WARP(kFullK0 + buf, (n >> 1) & 1);
         for (int i = tid - kFirstWeigh * 32; i < (kQ - len) * 8; i += 128) {
           const int at = (len + (i >> 3)) * 128 + (i & 7) * 16;
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -626,7 +693,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
       }
 #pragma unroll 1
       for (int pc = odd; pc < kPieces; pc += 2) {
-        const int st = pc % kStages, use = c * (kPieces / kStages) + pc / kStages;
+        const int st = pc % kStages, use = int(n) * (kPieces / kStages) + pc / kStages;
         uint32_t x[2][4], part[3][2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) ldmatrix_x4_t(x[i], v + pc * (kPiece * 128) + at[i]);
@@ -648,10 +715,10 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
         if (use > 0) DL_WAIT_WARP(kWFree0 + st, (use - 1) & 1);
         tc_fence_after();
 #pragma unroll
-        for (int n = 0; n < 3; ++n)
+        for (int q = 0; q < 3; ++q)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            tmem_st_16x8(tmem + kColW + st * kWStage + n * kWPart + lanes + (uint32_t(16 * i) << 16), part[n][i]);
+            tmem_st_16x8(tmem + kColW + st * kWStage + q * kWPart + lanes + (uint32_t(16 * i) << 16), part[q][i]);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&bars[kWFull0 + st], lane);
@@ -665,17 +732,22 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     const int row = quarter * 32 + lane;    // value row, lane of D
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
     const int hd = DV == 64 ? quarter >> 1 : 0;
-    const bool owns = h0 + hd < hend;
     const int p0 = DV == 64 ? (quarter & 1) * 32 : quarter * 32;  // the warp's first row of its head
-    const size_t head_off = (seq * p.H + h0 + hd) * size_t(DV) * DK + size_t(p0) * DK;
-    const size_t tile_off = (size_t(tile) * p.H + h0 + hd) * size_t(DV) * DK + p0 + lane;
     // The state comes and goes through D's place in TMEM: global rows are
     // touched 32 bytes by 4 lanes, the registers hold a row a lane.
+    unsigned n = 0;
+    DL_ITEMS(w) {
+    const bool owns = w.h0 + hd < w.hend;
+    const size_t head_off = (w.seq * p.H + w.h0 + hd) * size_t(DV) * DK + size_t(p0) * DK;
+    const size_t tile_off = (size_t(w.tile) * p.H + w.h0 + hd) * size_t(DV) * DK + p0 + lane;
     const size_t piece = head_off + size_t(lane >> 2) * DK + 2 * (lane & 3);
     float decay = 0.f;  // log2 of everything forgotten in this tile (STATES)
     float S[DK];
-    {
-      const bool ws = !STATES && owns && ntiles > 1, user = !STATES && owns && ntiles == 1 && p.S0 != nullptr;
+    if (STATES) {
+#pragma unroll
+      for (int i = 0; i < DK; ++i) S[i] = 0.f;
+    } else {
+      const bool ws = owns && w.cut, user = owns && !w.cut && p.S0 != nullptr;
       // all loads before the first store: one latency, not DK / 32
       float x[DK / 32][32];
       const uint32_t to = tmem + kColD + lanes;
@@ -719,16 +791,18 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
       for (int i = 0; i < DK / 8; ++i) put8(i);
       fence_async_smem();
     }
-    if (!STATES) warp_arrive(&bars[kSReady], lane);
-    for (int c = 0; c < nch; ++c) {
-      const uint32_t ph = uint32_t(c) & 1u;
-      const int buf = c & 1;
-      DL_WAIT_WARP(kWts0 + buf, (c >> 1) & 1);
+    if (!STATES && w.nch > 0) warp_arrive(&bars[kSReady], lane);
+    for (int c = 0; c < w.nch; ++c, ++n) {
+      const uint32_t ph = n & 1u;
+      const int buf = int(ph);
+      // the next item's state stands in for this one's last
+      const bool goes_on = STATES || c + 1 < w.nch;
+      DL_WAIT_WARP(kWts0 + buf, (n >> 1) & 1);
       const float tot = fT[buf * 2 + hd];
       const float keep = exp2f(tot);
       decay += tot;
       warp_arrive(&bars[kWtsFree0 + buf], lane);
-      DL_WAIT_WARP(kD0 + ph, (c >> 1) & 1);
+      DL_WAIT_WARP(kD0 + ph, (n >> 1) & 1);
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < DK / 16; ++b) {
@@ -737,22 +811,22 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[b * 16 + i] = fmaf(S[b * 16 + i], keep, x[i]);
-        if (!STATES) {  // Y, which reads the last one, was issued before D's end
+        if (!STATES && goes_on) {  // Y, which reads the last one, was issued before D's end
           put8(2 * b);
           put8(2 * b + 1);
         }
       }
       if (!STATES) fence_async_smem();
       tc_fence_before();
-      warp_arrive(&bars[STATES ? kSReady + ph : kSReady], lane);
+      if (goes_on) warp_arrive(&bars[STATES ? kSReady + ph : kSReady], lane);
     }
     if (STATES) {
       if (owns) {
 #pragma unroll
         for (int i = 0; i < DK; ++i) p.ws[tile_off + size_t(i) * DV] = S[i];
-        if (p0 + lane == 0) p.wdecay[size_t(tile) * p.H + h0 + hd] = decay;
+        if (p0 + lane == 0) p.wdecay[size_t(w.tile) * p.H + w.h0 + hd] = decay;
       }
-    } else if (owns && last_tile && p.S1 != nullptr) {
+    } else if (owns && w.last && p.S1 != nullptr) {
 #pragma unroll
       for (int b = 0; b < DK / 32; ++b)
         tmem_st32(tmem + kColD + b * 32 + lanes, *reinterpret_cast<float(*)[32]>(S + 32 * b));
@@ -772,6 +846,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
           *reinterpret_cast<float2*>(p.S1 + piece + size_t((i >> 3) * 16 + (i & 1) * 8) * DK + b * 32 +
                                      ((i >> 1) & 3) * 8) = make_float2(x[b][2 * i], x[b][2 * i + 1]);
     }
+    }
   } else if (!STATES) {
     // ----------------------------------------------------------- M and o
     take_registers<kElemRegs>();
@@ -780,23 +855,25 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
     // Y: 64 value columns of head slot hs
     const int hs = DV == 64 ? wg : 0;
-    const int h = h0 + hs;
-    const bool live = h < hend;
     const int col0 = DV == 64 ? 0 : wg * 64;
+    unsigned n = 0;
+    DL_ITEMS(w) {
+    const int h = w.h0 + hs;
+    const bool live = h < w.hend;
     const float dskip = live && p.d != nullptr ? p.d[h] : 0.f;
-    for (int c = 0; c < nch; ++c) {
-      const uint32_t ph = uint32_t(c) & 1u;
-      const int buf = c & 1;
-      const int t0 = begin + c * kQ;
-      const int len = min(kQ, end - t0);
-      DL_WAIT_WARP(kWts0 + buf, (c >> 1) & 1);
+    for (int c = 0; c < w.nch; ++c, ++n) {
+      const uint32_t ph = n & 1u;
+      const int buf = int(ph);
+      const int t0 = w.begin + c * kQ;
+      const int len = min(kQ, w.end - t0);
+      DL_WAIT_WARP(kWts0 + buf, (n >> 1) & 1);
       const float grow = ex2(fT[buf * 2 + hs] - fS[(buf * 2 + hs) * kQ + row]);
       float st[kHeads];
 #pragma unroll
       for (int e = 0; e < kHeads; ++e) st[e] = fS[(buf * 2 + e) * kQ + row];
       DL_WAIT_WARP(kG, ph);
       tc_fence_after();
-      if (c > 0) {  // by now the last chunk's outputs have left its value stage
+      if (n > 0) {  // by now the last chunk's outputs have left its value stage
         if (lane == 0) tma_store_read();
         warp_arrive(&bars[kVFree0 + (buf ^ 1)], lane);
       }
@@ -878,7 +955,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&bars[kMReady], lane);
-      DL_WAIT_WARP(kZ0 + ph, (c >> 1) & 1);
+      DL_WAIT_WARP(kZ0 + ph, (n >> 1) & 1);
       tc_fence_after();
       // through the warp's 32 rows of the value stage, whose last reader M V was:
       // whole boxes leave by TMA (a row a lane kept the store path busy for 3,000
@@ -914,10 +991,12 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
         }
       }
     }
+    }
   }
 done:
   __syncwarp();
   if (!STATES && warp < kElemWarps && lane == 0) tma_store_read();
+#undef DL_ITEMS
 #undef DL_WAIT
 #undef DL_WAIT_WARP
   __syncthreads();
@@ -950,7 +1029,7 @@ dl_ssm_join_kernel(const float* S0, float* ws, const float* wdecay, const __grid
   if (j1 - j0 < 2) return;
   float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
   if (S0 != nullptr) {
-    const float* src = S0 + ((size_t(seq0) + sl) * H + h) * size_t(floats) + size_t(at % dv) * dk + at / dv;
+    const float* src = S0 + ((size_t(seq0) + seqs.index(sl)) * H + h) * size_t(floats) + size_t(at % dv) * dk + at / dv;
     e = make_float4(src[0], src[dk], src[2 * dk], src[3 * dk]);
   }
   for (int j = j0; j < j1; ++j) {
@@ -999,11 +1078,11 @@ bool encode_rows(CUtensorMap* m, const void* base, long long rows, int cols, lon
 }
 
 template <int DK, int DV, bool STATES, int NS>
-cudaError_t launch_chunk(const TcParams& p, const SeqTable<NS>& tab, int seq0, unsigned grid,
+cudaError_t launch_chunk(const TcParams& p, const OrderedSeqs<NS>& tab, int seq0, unsigned grid,
                          const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& o, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  auto kern = dl_ssm_chunk_kernel<DK, DV, STATES, SeqTable<NS>>;
+  auto kern = dl_ssm_chunk_kernel<DK, DV, STATES, OrderedSeqs<NS>>;
   // the roles' register shares add up against what the block starts with
   static std::atomic<int> regs{0};
   if (regs.load(std::memory_order_relaxed) == 0) {
@@ -1023,10 +1102,14 @@ cudaError_t launch_chunk(const TcParams& p, const SeqTable<NS>& tab, int seq0, u
 template <int DK, int DV, int NS>
 cudaError_t launch_range(const SsmParams& sp, TcParams p, int seq0, int n, const int32_t* starts,
                          const SsmPlan& plan, void* ws, cudaStream_t s) {
-  SeqTable<NS> tab;
-  const long long tiles = fill_seqs(tab, starts, seq0, n, plan.tile_tokens);
-  const long long grid = tiles * p.pairs;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  OrderedSeqs<NS> tab;
+  const long long tiles = fill_ordered(tab, starts, seq0, n, plan.tile_tokens);
+  const long long items = tiles * p.pairs;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidConfiguration;
+  const long long grid = items < sms ? items : sms;  // one CTA an SM
+  p.items = unsigned(items);
   p.ws = static_cast<float*>(ws);
   p.wdecay = p.ws + size_t(tiles) * p.H * DV * DK;
   CUtensorMap q, k, v, o;
@@ -1123,19 +1206,19 @@ size_t ssm_tile_bytes(int H, int dk, int dv, int n, const int32_t* starts, int t
   return any ? size_t(most) * H * (size_t(dv) * dk + 1) * 4 : 0;
 }
 
-template <int NS>
-cudaError_t launch_ssm_join(const SsmParams& p, float* ws, const float* wdecay, const SeqTable<NS>& tab,
-                            int seq0, int n, int dk, int dv, cudaStream_t s) {
+template <typename Table>
+cudaError_t launch_ssm_join(const SsmParams& p, float* ws, const float* wdecay, const Table& tab, int seq0,
+                            int n, int dk, int dv, cudaStream_t s) {
   const long long blocks = (long long)n * p.H * (dv * dk / 1024);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  dl_ssm_join_kernel<SeqTable<NS>><<<unsigned(blocks), 256, 0, s>>>(p.S0, ws, wdecay, tab, seq0, p.H, dk, dv);
+  dl_ssm_join_kernel<Table><<<unsigned(blocks), 256, 0, s>>>(p.S0, ws, wdecay, tab, seq0, p.H, dk, dv);
   count_launches(1);
   return cudaGetLastError();
 }
-template cudaError_t launch_ssm_join<kSmallSeqs>(const SsmParams&, float*, const float*, const SeqTable<kSmallSeqs>&,
-                                                 int, int, int, int, cudaStream_t);
-template cudaError_t launch_ssm_join<kLargeSeqs>(const SsmParams&, float*, const float*, const SeqTable<kLargeSeqs>&,
-                                                 int, int, int, int, cudaStream_t);
+template cudaError_t launch_ssm_join(const SsmParams&, float*, const float*, const SeqTable<kSmallSeqs>&, int, int,
+                                     int, int, cudaStream_t);
+template cudaError_t launch_ssm_join(const SsmParams&, float*, const float*, const SeqTable<kLargeSeqs>&, int, int,
+                                     int, int, cudaStream_t);
 
 cudaError_t launch_ssm_chunked(const SsmParams& sp, int n, const int32_t* starts, int dk, int dv,
                                const SsmPlan& plan, void* ws, cudaStream_t s) {
