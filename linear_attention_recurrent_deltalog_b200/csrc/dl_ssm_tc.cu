@@ -1032,17 +1032,26 @@ dl_ssm_join_kernel(const float* S0, float* ws, const float* wdecay, const __grid
     const float* src = S0 + ((size_t(seq0) + seqs.index(sl)) * H + h) * size_t(floats) + size_t(at % dv) * dk + at / dv;
     e = make_float4(src[0], src[dk], src[2 * dk], src[3 * dk]);
   }
-  for (int j = j0; j < j1; ++j) {
-    float4* w = reinterpret_cast<float4*>(ws + (size_t(j) * H + h) * size_t(floats) + at);
-    if (j + 1 == j1) {
-      *w = e;
-      break;
-    }
-    const float4 own = *w;
-    const float k = exp2f(wdecay[size_t(j) * H + h]);
-    *w = e;
-    e = make_float4(fmaf(e.x, k, own.x), fmaf(e.y, k, own.y), fmaf(e.z, k, own.z), fmaf(e.w, k, own.w));
+  auto at_tile = [&](int j) { return reinterpret_cast<float4*>(ws + (size_t(j) * H + h) * size_t(floats) + at); };
+  constexpr int U = 4;  // tiles in flight
+  for (int j = j0; j + 1 < j1; j += U) {
+    float4 own[U];
+    float k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j + u + 1 < j1) {
+        own[u] = *at_tile(j + u);
+        k[u] = exp2f(wdecay[size_t(j + u) * H + h]);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j + u + 1 < j1) {
+        *at_tile(j + u) = e;
+        e = make_float4(fmaf(e.x, k[u], own[u].x), fmaf(e.y, k[u], own[u].y), fmaf(e.z, k[u], own[u].z),
+                        fmaf(e.w, k[u], own[u].w));
+      }
   }
+  *at_tile(j1 - 1) = e;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
