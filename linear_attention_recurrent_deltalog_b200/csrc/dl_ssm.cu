@@ -314,19 +314,20 @@ cudaError_t launch_ssm_step(const SsmParams& p, int B, int dk, int dv, bool bf16
   return dispatch_shape(Shape{dk, dv, bf16 ? 1 : 0, 1}, RunStep{p, B, s});
 }
 
-// Tile length: a warp an SM quarter already hides most of its latency, so
-// sequences are cut only where that leaves a third of the device or less busy
-// (the cut reads k and v twice and costs two launches).
+// Tile length: with two CTAs an SM most of the latency is hidden, so a call
+// takes about its tokens spread over as many, or its longest sequence.  Where the
+// latter is three times the former or more, sequences are cut to the former's
+// length (the cut reads k and v twice and costs two launches).
 SsmPlan plan_ssm_scan(int H, int dk, int dv, int n, const int32_t* starts, int sms) {
-  constexpr int kMinTile = 64;
+  constexpr long long kMinTile = 64;
   long long longest = 0;
   for (int i = 0; i < n; ++i) {
     const long long t = (long long)starts[i + 1] - starts[i];
     longest = t > longest ? t : longest;
   }
-  const long long ctas = (long long)n * H * (dv / kScanRows);
-  long long parts = ctas > 0 ? 2LL * sms / ctas : 1;
-  parts = parts < longest / kMinTile ? parts : longest / kMinTile;
+  const long long total = n > 0 ? (long long)starts[n] - starts[0] : 0;
+  const long long spread = total * H * (dv / kScanRows) / (2LL * sms);
+  long long parts = longest / (spread > kMinTile ? spread : kMinTile);
   if (parts < 3) parts = 1;
   const long long len = (longest + parts - 1) / parts;
   const long long tile = (len + kScanTile - 1) / kScanTile * kScanTile;

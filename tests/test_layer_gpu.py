@@ -55,6 +55,19 @@ def test_conv_prompt(dtype, C, W, act, lens):
     assert (y[T:] == 7).all()
 
 
+def test_conv_prompt_of_many_rows_a_thread():
+    # enough rows that a thread walks down more than one batch of them, and
+    # sequences that end inside a batch
+    C, W, st = 1536, 4, starts_of([1, 2985, 3, 31])
+    x, w, b = rnd(1, 3020, C).to(T16), rnd(2, C, W), rnd(3, C)
+    h = rnd(4, 4, W - 1, C).to(T16)
+    y, h1 = torch.empty(3020, C, dtype=T16, device="cuda"), torch.empty_like(h, device="cuda")
+    dl.dl_conv_prompt(dl.ConvConfig(C, W, "bf16"), st, x.cuda(), w.cuda(), b.cuda(), h.cuda(), h1, y)
+    want, mag, hw = ref.conv(x, st, w, b, h, True)
+    close(y, want, ref.conv_tol(mag, W, T16), "y")
+    assert torch.equal(h1.double().cpu(), hw)
+
+
 def test_conv_strides_in_place_state_and_no_state():
     # channel ranges of wider rows; x with an odd stride takes the narrow path
     C, W, st = 64, 4, starts_of([9, 0, 40])
@@ -189,6 +202,37 @@ def test_ssm_prompt_long_and_uneven(dtype):
     st = starts_of([2900, 70])
     z = ssm_inputs(40, 2970, 2, 2, 1, 128, 64, dtype)
     check_prompt(dl.SsmConfig(2, 1, 128, 64, dtype), st, z)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,G,dk,dv", [(2, 1, 64, 128), (10, 2, 64, 64)])
+def test_ssm_prompt_many_sequences_some_cut(dtype, H, G, dk, dv):
+    # more sequences than the small table holds, empty ones among them, some
+    # long enough to be cut, and several work items for each block of threads
+    lens = [int(v) for v in np.random.default_rng(4).integers(0, 6, 80)]
+    lens[7], lens[50], lens[79] = 1500, 130, 300
+    st = starts_of(lens)
+    z = ssm_inputs(45, int(st[-1]), len(lens), H, G, dk, dv, dtype, pad=1)
+    cfg = dl.SsmConfig(H, G, dk, dv, dtype)
+    assert dl.dl_ssm_bytes(cfg, st) > 0
+    o, s1 = check_prompt(cfg, st, z, pad=1)
+    oi, si = run_prompt(cfg, st, z, in_place=True, pad=1)
+    assert torch.equal(o, oi) and torch.equal(s1, si)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ssm_prompt_states_aligned_to_16_bytes_only(dtype):
+    st = starts_of([150, 20])
+    z = ssm_inputs(47, 170, 2, 2, 1, 128, 64, dtype)
+    cfg = dl.SsmConfig(2, 1, 128, 64, dtype)
+    o, s1 = run_prompt(cfg, st, z)
+    g = {k: v.cuda() for k, v in z.items()}
+    n = z["S0"].numel()
+    S0, S1 = (torch.empty(n + 4, device="cuda")[4:].view(z["S0"].shape) for _ in range(2))
+    S0.copy_(g["S0"])
+    o2 = torch.empty_like(o)
+    dl.dl_ssm_prompt(cfg, st, g["q"], g["k"], g["v"], g["dt"], g["a"], g["d"], g["bias"], S0, S1, o2)
+    assert torch.equal(o, o2) and torch.equal(s1, S1)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -358,6 +402,13 @@ def test_norm_zero_tiny_and_bad_rows():
     assert torch.isfinite(o[4]).all()
 
 
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("rows,D", [(2500, 4096), (9000, 520)])
+def test_norm_several_rows_a_team(rows, D, block):
+    # more rows than run at once: a team takes one after the other
+    check_norm(rows, D, "bf16", "e4m3", block, res=True)
+
+
 def test_norm_many_rows():
     # more rows than one dimension of blocks of the short-row kernel covers evenly
     check_norm(70001, 24, "f32", "bf16", 0, res=False)
@@ -431,6 +482,37 @@ def test_prompt_in_a_graph_and_twice_the_same():
     torch.cuda.synchronize()
     for o, s in outs[1:]:
         assert torch.equal(o, outs[0][0]) and torch.equal(s, outs[0][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompts_at_the_same_time(dtype):
+    # two streams, a workspace each
+    st = [starts_of([900, 40]), starts_of([30, 1200])]
+    cfg = dl.SsmConfig(2, 1, 128, 64, dtype)
+    z = [{k: v.cuda() for k, v in ssm_inputs(97 + i, int(s[-1]), 2, 2, 1, 128, 64, dtype).items()}
+         for i, s in enumerate(st)]
+    ws = [torch.empty(dl.dl_ssm_bytes(cfg, s), dtype=torch.uint8, device="cuda") for s in st]
+    alone = [(torch.empty(int(s[-1]), 2, 64, dtype=DT[dtype], device="cuda"), torch.empty_like(u["S0"]))
+             for s, u in zip(st, z)]
+    both = [[torch.empty_like(v) for v in pair] for pair in alone]
+
+    def call(i, out):
+        u = z[i]
+        dl.dl_ssm_prompt(cfg, st[i], u["q"], u["k"], u["v"], u["dt"], u["a"], u["d"], u["bias"], u["S0"],
+                         out[1], out[0], ws[i])
+
+    for i in range(2):
+        call(i, alone[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(i, both[i])
+    torch.cuda.synchronize()
+    assert dl.dl_device_error(None) == (0, 0)
+    for a, b in zip(alone, both):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 # ------------------------------------------------------------ empty calls
