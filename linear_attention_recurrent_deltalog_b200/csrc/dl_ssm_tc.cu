@@ -13,23 +13,27 @@
 //     Y = Q S^T            [t, p]   B: the state as bf16, written by its owners
 //     Y = grow o Y + M V   [t, p]   A: M as bf16 in TMEM, B: V, MN-major
 //     D = (w o V)^T K      [p, n]   A: w o V in TMEM as three bf16 parts, B: K, MN-major
-// Rounding: the state is carried in fp32 registers (one thread per value
-// row) and w o V enters D as hi + mid + lo, all 24
-// bits, so S' is right to fp32 rounding; only what feeds the bf16 output o is
-// rounded to bf16 on the way, each term once (M, or the state that q reads),
-// which is of the size of o's own rounding.
+// Rounding: the state is carried in fp32 registers (one thread per value row)
+// and w o V enters D as hi + mid + lo, all 24 bits, so S' is right to fp32
+// rounding; only what feeds the bf16 output o is rounded to bf16 on the way, each
+// term once (M, or the state that q reads), which is of the size of o's own
+// rounding (0.0023 of o's norm in all, 0.0017 of it the output's).
 //
-// A CTA owns 128 value columns (two neighbouring heads of a group at d_v = 64,
-// which share G and the loads of q and k; one head at 128) and walks the
-// chunks of one tile of one sequence.  Long sequences are cut into tiles when
-// there are too few CTAs: a first launch (STATES) forms every tile's own state
-// from zero, dl_ssm_join_kernel turns those into the state each tile enters
-// with, and the main launch starts from them.
+// A work item is 128 value columns (two neighbouring heads of a group at d_v =
+// 64, which share G and the loads of q and k; one head at 128) over the chunks of
+// one tile of one sequence; a CTA an SM walks over its items, the next one's
+// loads in flight.  Long sequences are cut into tiles when there are too few
+// items: a first launch (STATES) forms every tile's own state from zero,
+// dl_ssm_join_kernel turns those into the state each tile enters with, and the
+// main launch starts from them.
 //
-// What bounds a chunk is shared memory (an MMA with both operands there reads
-// 128 bytes a cycle, all it can deliver), which is why M and w o V are TMEM
-// operands: with w o V in shared memory its parts were written once and read,
-// with K, three times over, 0.3 MB more a chunk.
+// T = 8192, H = 64, d = 128 x 64, one sequence in four tiles: 115 us, of which the
+// states take 38 (2.4 a chunk), the join 6 and the main launch 76 (4.8 a chunk,
+// 1.7 of them its MMAs').  What bounds a chunk is the element work: 4,000 of a
+// scheduler's 7,500 cycles issue an instruction, the tensor pipe is busy for 0.45
+// of them.  M and w o V are TMEM operands because shared memory is next: an MMA
+// with both operands there reads 128 bytes a cycle, all it can deliver, and w o V
+// there, written once and read with K three times over, cost 0.3 MB more a chunk.
 //
 // Warps 0-7: M and o (warp w reaches TMEM lanes 32 (w mod 4) ..).  Warps 8-11:
 // the state, a value row a thread.  Warps 12-19: w o V, 16 tokens at a time.
@@ -1155,7 +1159,7 @@ int cta_pairs(int H, int G, int dv) {
 }  // namespace
 
 // Tile length: one CTA runs per SM, and a cut tile costs a second walk over
-// its k and v (kStatesCost of a full one: 1.9 of 3.9 us a chunk), so take the length whose
+// its k and v (kStatesCost of a full one: 2.4 of 4.8 us a chunk), so take the length whose
 // waves of CTAs finish first.
 SsmPlan plan_ssm(int H, int G, int dk, int dv, int n, const int32_t* starts, int sms) {
   constexpr double kStatesCost = 0.5, kTileCost = 1.0;  // in chunks
