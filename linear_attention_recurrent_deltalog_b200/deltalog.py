@@ -316,10 +316,14 @@ def _flat(t, name: str, numel: int, dtype: torch.dtype) -> Optional[int]:
     """The same for a tensor (or None); returns its address."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
-        _need(t, name, numel, dtype)
+    _need(t, name, numel, dtype)
     return t.data_ptr()
 
 
@@ -344,16 +348,23 @@ def _rows(t, name: str, rows: int, cols: int, dtype: torch.dtype) -> int:
     """Checks a tensor of at least ``rows`` rows of ``cols`` elements and
     returns its row stride: [rows, cols], or [rows, a, b] with a * b = cols,
     whose rows may lie apart but are contiguous themselves."""
+    try:  # the common case first: the checks cost as much as a small kernel
+        if t.dtype is dtype:
+            n, width = t.shape
+            ld, unit = t.stride()
+            if width == cols and unit == 1 and n >= rows and (ld >= cols or n <= 1):
+                return ld if n > 1 else cols  # a single row's stride is never used
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     shape, ld = t.shape, t.stride()
+    n = shape[0] if shape else 0
     if len(shape) == 2:
-        n, width = shape
-        ok = width == cols and (ld[1] == 1 or cols == 1)
+        ok = shape[1] == cols and (ld[1] == 1 or cols == 1)
     else:
-        n = shape[0] if shape else 0
         ok = len(shape) == 3 and shape[1] * shape[2] == cols and \
             (n == 0 or t[0].is_contiguous())
     if not ok:
@@ -362,19 +373,25 @@ def _rows(t, name: str, rows: int, cols: int, dtype: torch.dtype) -> int:
     if n < rows:
         raise ValueError(f"{name}: {n} rows, need {rows}")
     if n <= 1:
-        return cols  # the one row's stride is never used
+        return cols
     if ld[0] < cols:
         raise ValueError(f"{name}: rows overlap (stride {ld[0]}, {cols} elements)")
     return ld[0]
 
 
-def _on_device(names: str, *tensors) -> None:
+def _on_device(names: str, *tensors) -> Optional[int]:
     """Every tensor (or None) on the current CUDA device, whose stream the call uses."""
     dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
     for t in tensors:
         if t is not None and t.get_device() != dev:
             name = names.split()[[x is t for x in tensors].index(True)]
             raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+    return dev
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The given stream's handle, or the current one's of the current device ``dev``."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 _INT32 = np.dtype(np.int32)
@@ -470,9 +487,9 @@ def dl_conv_prompt(cfg: ConvConfig, starts, x, w, bias, h0, h1, y, stream=None) 
     pb = _flat(bias, "bias", C, torch.float32)
     ph0 = _flat(h0, "h0", n * (W - 1) * C, t)
     ph1 = _flat(h1, "h1", n * (W - 1) * C, t)
-    _on_device("x w bias h0 h1 y", x, w, bias, h0, h1, y)
+    dev = _on_device("x w bias h0 h1 y", x, w, bias, h0, h1, y)
     rc = _lib.dl_conv_prompt(cfg.ref, n, at, x.data_ptr(), ldx, pw, pb, ph0, ph1,
-                             y.data_ptr(), ldy, _stream(stream))
+                             y.data_ptr(), ldy, _stream_on(dev, stream))
     if rc:
         _check(rc, "dl_conv_prompt")
 
@@ -488,9 +505,9 @@ def dl_conv_step(cfg: ConvConfig, x, w, bias, h, y, stream=None) -> None:
     pw = _flat(w, "w", C * W, torch.float32)
     pb = _flat(bias, "bias", C, torch.float32)
     ph = _flat(h, "h", B * (W - 1) * C, t)
-    _on_device("x w bias h y", x, w, bias, h, y)
+    dev = _on_device("x w bias h y", x, w, bias, h, y)
     rc = _lib.dl_conv_step(cfg.ref, B, x.data_ptr(), ldx, pw, pb, ph, y.data_ptr(), ldy,
-                           _stream(stream))
+                           _stream_on(dev, stream))
     if rc:
         _check(rc, "dl_conv_step")
 
@@ -505,7 +522,7 @@ def dl_ssm_bytes(cfg: SsmConfig, starts) -> int:
 
 
 def _ssm_io(cfg: SsmConfig, rows: int, n: int, q, k, v, dt, a, d, dt_bias, o, S0, S1):
-    """-> (dl_ssm_io as bytes, addresses of S0 and S1)"""
+    """-> (dl_ssm_io as bytes, addresses of S0 and S1, the device)"""
     t, H, f32 = cfg.torch_in_dtype, cfg.H, torch.float32
     nk, nv = cfg.G * cfg.d_k, H * cfg.d_v
     ldq, ldk = _rows(q, "q", rows, nk, t), _rows(k, "k", rows, nk, t)
@@ -516,9 +533,9 @@ def _ssm_io(cfg: SsmConfig, rows: int, n: int, q, k, v, dt, a, d, dt_bias, o, S0
     pa, pd, pb = _flat(a, "a", H, f32), _flat(d, "d", H, f32), _flat(dt_bias, "dt_bias", H, f32)
     p0 = _flat(S0, "S0", n * nv * cfg.d_k, f32)
     p1 = _flat(S1, "S1", n * nv * cfg.d_k, f32)
-    _on_device("q k v dt a d dt_bias o S0 S1", q, k, v, dt, a, d, dt_bias, o, S0, S1)
+    dev = _on_device("q k v dt a d dt_bias o S0 S1", q, k, v, dt, a, d, dt_bias, o, S0, S1)
     return _pack_ssm_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), pa, pd or 0,
-                        pb or 0, o.data_ptr(), ldq, ldk, ldv, lddt, ldo), p0, p1
+                        pb or 0, o.data_ptr(), ldq, ldk, ldv, lddt, ldo), p0, p1, dev
 
 
 def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o, workspace=None,
@@ -528,7 +545,7 @@ def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o,
     after.  ``workspace``: a uint8 tensor of ``dl_ssm_bytes`` (allocated for
     the call when None)."""
     at, n, rows, keep = _starts(starts)
-    io, p0, p1 = _ssm_io(cfg, rows, n, q, k, v, dt, a, d, dt_bias, o, S0, S1)
+    io, p0, p1, dev = _ssm_io(cfg, rows, n, q, k, v, dt, a, d, dt_bias, o, S0, S1)
     if workspace is None:
         workspace = torch.empty(dl_ssm_bytes(cfg, keep), dtype=torch.uint8, device=q.device)
     elif not isinstance(workspace, torch.Tensor):
@@ -538,7 +555,7 @@ def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o,
         raise ValueError("workspace: must be contiguous")
     _on_device("workspace", workspace)
     rc = _lib.dl_ssm_prompt(cfg.ref, n, at, io, p0, p1,
-                            workspace.data_ptr() if nb else None, nb, _stream(stream))
+                            workspace.data_ptr() if nb else None, nb, _stream_on(dev, stream))
     if rc:
         _check(rc, "dl_ssm_prompt")
 
@@ -549,8 +566,8 @@ def dl_ssm_step(cfg: SsmConfig, q, k, v, dt, a, d, dt_bias, S, o, stream=None) -
     B = q.shape[0]
     if S is None:
         raise TypeError("S: expected a torch.Tensor")
-    io, p, _ = _ssm_io(cfg, B, B, q, k, v, dt, a, d, dt_bias, o, S, None)
-    rc = _lib.dl_ssm_step(cfg.ref, B, io, p, _stream(stream))
+    io, p, _, dev = _ssm_io(cfg, B, B, q, k, v, dt, a, d, dt_bias, o, S, None)
+    rc = _lib.dl_ssm_step(cfg.ref, B, io, p, _stream_on(dev, stream))
     if rc:
         _check(rc, "dl_ssm_step")
 
@@ -573,9 +590,9 @@ def dl_norm(cfg: NormConfig, x, w, out, res=None, res_out=None, scales=None, str
     if scales is None and cfg.out_dtype == "e4m3":
         raise TypeError("scales: expected a torch.Tensor for an e4m3 output")
     ps = _flat(scales, "scales", rows * cfg.scales_per_row, torch.float32)
-    _on_device("x w out res res_out scales", x, w, out, res, res_out, scales)
+    dev = _on_device("x w out res res_out scales", x, w, out, res, res_out, scales)
     rc = _lib.dl_norm(cfg.ref, rows, x.data_ptr(), ldx, pr, ldr, pw, pro, ldro, out.data_ptr(), ldo,
-                      ps, _stream(stream))
+                      ps, _stream_on(dev, stream))
     if rc:
         _check(rc, "dl_norm")
 
