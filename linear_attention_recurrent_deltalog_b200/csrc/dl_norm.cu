@@ -271,6 +271,7 @@ cudaError_t norm_by_length(const NormParams& p, cudaStream_t s) {
   if (p.D <= 128) return norm_t<T, TO, 16, 1, VEC>(p, s);
   if (p.D <= 256) return norm_t<T, TO, 32, 1, VEC>(p, s);
   if (p.D <= 512) return norm_t<T, TO, 32, 2, VEC>(p, s);
+  if (p.D <= 1024) return norm_t<T, TO, 128, 1, VEC>(p, s);
   if (p.D <= 2048) return norm_t<T, TO, 128, 2, VEC>(p, s);
   if (p.D <= 4096) return norm_t<T, TO, 256, 2, VEC>(p, s);
   if (p.D <= 8192) return norm_t<T, TO, 512, 2, VEC>(p, s);
