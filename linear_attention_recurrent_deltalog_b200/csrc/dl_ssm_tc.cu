@@ -153,6 +153,7 @@ struct TcParams {
   long long lddt, ldo;
   int H, G, softplus;
   int pairs;        // work items per tile
+  int hpg, ppg;     // heads and items of a group
   int tile_tokens;
   unsigned items;   // tiles * pairs
 };
@@ -417,7 +418,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
   auto work = [&](unsigned item) {
     Work w;
     w.tile = int(item / unsigned(p.pairs));
-    const int pair = int(item % unsigned(p.pairs));
+    const int pair = int(item - unsigned(w.tile) * unsigned(p.pairs));
     const int sl = seqs.find(w.tile);
     const int first = seqs.tile0[sl], ntiles = seqs.tile0[sl + 1] - first;
     w.begin = seqs.begin[sl] + (w.tile - first) * p.tile_tokens;
@@ -426,10 +427,9 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     w.cut = ntiles > 1;
     w.last = w.tile - first == ntiles - 1;
     // pairs run through the heads of a group
-    const int hpg = p.H / p.G, ppg = (hpg + kHeads - 1) / kHeads;
-    w.g = pair / ppg;
-    w.h0 = w.g * hpg + (pair % ppg) * kHeads;
-    w.hend = (w.g + 1) * hpg;
+    w.g = p.G > 1 ? pair / p.ppg : 0;
+    w.h0 = w.g * p.hpg + (pair - w.g * p.ppg) * kHeads;
+    w.hend = (w.g + 1) * p.hpg;
     w.seq = size_t(seq0) + size_t(seqs.index(sl));
     return w;
   };
@@ -1250,6 +1250,8 @@ cudaError_t launch_ssm_chunked(const SsmParams& sp, int n, const int32_t* starts
   p.G = sp.G;
   p.softplus = sp.softplus;
   p.pairs = cta_pairs(sp.H, sp.G, dv);
+  p.hpg = sp.H / sp.G;
+  p.ppg = p.pairs / sp.G;
   p.tile_tokens = plan.tile_tokens;
   if (dk == 128) return dv == 64 ? launch_tc<128, 64>(sp, p, n, starts, plan, ws, s)
                                  : launch_tc<128, 128>(sp, p, n, starts, plan, ws, s);
