@@ -27,7 +27,7 @@
 // dl_ssm_join_kernel turns those into the state each tile enters with, and the
 // main launch starts from them.
 //
-// T = 8192, H = 64, d = 128 x 64, one sequence in four tiles: 115 us, of which the
+// T = 8192, H = 64, d = 128 x 64, one sequence in four tiles: 114 us, of which the
 // states take 38 (2.4 a chunk), the join 6 and the main launch 76 (4.8 a chunk,
 // 1.7 of them its MMAs').  What bounds a chunk is the element work: 4,000 of a
 // scheduler's 7,500 cycles issue an instruction, the tensor pipe is busy for 0.45
