@@ -111,6 +111,8 @@ __device__ __forceinline__ void store8(__nv_fp8_e4m3* row, int c, int D, const f
   }
 }
 
+constexpr float kSmallAmax = 0x1p-64f, kSmallUp = 0x1p64f;
+
 // The larger magnitude; a NaN on either side stays.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -230,7 +232,14 @@ dl_norm_kernel(const NormParams p) {
       for (int v = 0; v < V; ++v) {
         const float amax = p.block == 0 ? rowmax : m[v];
         const bool zero = amax < kTinyAmax;
-        const float inv = zero ? 0.f : __fdiv_rn(448.f, amax);
+        // 448 / amax leaves fp32's range from amax = 1.75 * 2^-120 down: small
+        // blocks are brought up by a power of two first, which rounds nothing
+        const bool small = amax < kSmallAmax;
+        if (small) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[v][e] *= kSmallUp;
+        }
+        const float inv = zero ? 0.f : __fdiv_rn(448.f, small ? amax * kSmallUp : amax);
         const int first = VEC ? c[v] : c[v] - (i & 15) + (i & 15) * 8;  // as if it held 8 neighbours
         if (p.block == 0 ? first == 0 : (first % 128 == 0 && first < D))
           p.scales[row * nblk + (p.block == 0 ? 0 : first / 128)] = zero ? 0.f : __fdiv_rn(amax, 448.f);

@@ -1,0 +1,80 @@
+"""The operators around the recurrent step on the GPU at the borders of their
+number formats and of their launch forms, against 64-bit definitions."""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+from linear_attention_recurrent_deltalog_b200 import deltalog as dl
+
+pytestmark = pytest.mark.gpu
+
+T16, T32, T8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+U = 2.0 ** -24
+
+
+def rnd(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+# ------------------------------------------------------------------ norm
+
+# largest magnitudes of a block around the ones where 448 / amax leaves fp32's
+# range (below 1.75 * 2^-120) and where a block is stored as zeros (below 2^-120)
+PEAKS = [2.0 ** -121, 2.0 ** -120 * (1 - U), 2.0 ** -120, 1.2 * 2.0 ** -120, 1.74 * 2.0 ** -120,
+         1.75 * 2.0 ** -120, 2.0 ** -119, 1.5 * 2.0 ** -100, 2.0 ** -65, 1.1 * 2.0 ** -64, 1.0, 2.0 ** 100]
+
+
+def peaked(n, peak, seed):
+    """n values whose largest magnitude is `peak`: zeros, the peak, and values down to its 2^-20."""
+    g = torch.Generator().manual_seed(seed)
+    v = peak * torch.exp2(-20 * torch.rand(n, generator=g)) * torch.sign(torch.randn(n, generator=g))
+    v[::5] = 0.0
+    v[1] = -peak
+    return v.to(T32)
+
+
+def check_codes(codes, scale, n):
+    """Codes and scale of one block of exact values n: the scale is amax / 448
+    rounded once (half a step: 2^-24 of it, or of the smallest normal below
+    that); a code's value is n * (448 / amax) after two roundings to 24 bits,
+    then half a step of e4m3 (2^-4 of it, at least half of 2^-9)."""
+    n = n.double()
+    amax = float(n.abs().max())
+    codes = codes.double()
+    assert torch.isfinite(codes).all()
+    if amax < 2.0 ** -120:
+        assert (codes == 0).all() and float(scale) == 0.0
+        return
+    assert abs(float(scale) - amax / 448) <= amax / 448 * U + 2.0 ** -150
+    want = n * (448 / amax)
+    pre = want.abs() * 2.1 * U
+    assert ((codes - want).abs() <= torch.clamp((want.abs() + pre) * 2.0 ** -4, min=2.0 ** -10) + pre).all()
+    assert (codes[n == 0] == 0).all() and float(codes.abs().max()) == 448.0
+
+
+@pytest.mark.parametrize("tail", [0, 3])  # 3: rows that take the element-wise path
+def test_norm_codes_of_small_blocks(tail):
+    # rows of ones and eps = 0 have the root 1 exactly: n is the weight
+    D = 128 * len(PEAKS) + tail
+    w = torch.cat([peaked(128, p, i) for i, p in enumerate(PEAKS)] +
+                  ([peaked(tail, 1.0, 99)] if tail else []))
+    out, sc = torch.empty(2, D, dtype=T8, device="cuda"), torch.empty(2, -(-D // 128), device="cuda")
+    dl.dl_norm(dl.NormConfig(D, "f32", "e4m3", block=128, eps=0.0), torch.ones(2, D, device="cuda"), w.cuda(),
+               out, scales=sc)
+    o, sc = out.float().cpu(), sc.cpu()
+    for row in range(2):
+        for b in range(len(PEAKS)):
+            check_codes(o[row, 128 * b:128 * b + 128], sc[row, b], w[128 * b:128 * b + 128])
+
+
+@pytest.mark.parametrize("D", [64, 1024, 4099])
+@pytest.mark.parametrize("peak", PEAKS)
+def test_norm_codes_of_small_rows(peak, D):
+    w = peaked(D, peak, 7)
+    out, sc = torch.empty(3, D, dtype=T8, device="cuda"), torch.empty(3, 1, device="cuda")
+    dl.dl_norm(dl.NormConfig(D, "bf16", "e4m3", eps=0.0), torch.ones(3, D, dtype=T16, device="cuda"), w.cuda(),
+               out, scales=sc)
+    for row in range(3):
+        check_codes(out[row].float().cpu(), sc[row].cpu(), w)
