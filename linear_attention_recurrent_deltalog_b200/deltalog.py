@@ -394,6 +394,22 @@ def _stream_on(dev: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """Memory for one call on ``stream``, from that stream's pool: what it held before and what it
+    is given to afterwards then run before and after the call."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = _stream(stream)
+        if stream == 2:  # the per-thread default stream: another one in every thread
+            raise ValueError("workspace: needed on the per-thread default stream")
+        # 0 and 1 both name the legacy default stream
+        stream = torch.cuda.default_stream(device) if stream < 2 else \
+            torch.cuda.ExternalStream(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 _INT32 = np.dtype(np.int32)
 
 
@@ -543,11 +559,11 @@ def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o,
     """Selective state space scan of packed sequences; ``S0`` (or None) and
     ``S1`` (or None, or ``S0``) are the states [n, H, d_v, d_k] before and
     after.  ``workspace``: a uint8 tensor of ``dl_ssm_bytes`` (allocated for
-    the call when None)."""
+    the call, on its stream, when None)."""
     at, n, rows, keep = _starts(starts)
     io, p0, p1, dev = _ssm_io(cfg, rows, n, q, k, v, dt, a, d, dt_bias, o, S0, S1)
     if workspace is None:
-        workspace = torch.empty(dl_ssm_bytes(cfg, keep), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(dl_ssm_bytes(cfg, keep), q.device, stream)
     elif not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace: expected a torch.Tensor")
     nb = workspace.numel() * workspace.element_size()

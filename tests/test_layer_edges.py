@@ -1,0 +1,85 @@
+"""Host side of the operators around the recurrent step at the borders of
+what they accept: no GPU is needed, fakes stand in for streams and the library."""
+
+from __future__ import annotations
+
+import contextlib
+import types
+
+import pytest
+import torch
+
+from linear_attention_recurrent_deltalog_b200 import deltalog as dl
+
+
+# ------------------------------------------- the workspace of a prompt's scan
+
+class FakeStream:
+    device_index = 0
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def fake_device(monkeypatch):
+    """A device 0 whose current stream is 11 until torch.cuda.stream() says
+    otherwise; records (stream of the call, stream its workspace came from)."""
+    now, made, calls = [11], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        now.append(stream.cuda_stream)
+        yield
+        now.pop()
+
+    empty = torch.empty
+
+    def allocate(*a, **kw):
+        made.append(now[-1])
+        return empty(*a, **kw)
+
+    def bytes_(cfg, n, at, out):
+        out._obj.value = 512
+        return 0
+
+    def prompt(cfg, n, at, io, s0, s1, ws, nbytes, stream):
+        assert ws and nbytes == 512
+        calls.append((stream, made[-1]))
+        return 0
+
+    monkeypatch.setattr(dl, "_on_device", lambda names, *t: 0)
+    monkeypatch.setattr(dl, "_lib", types.SimpleNamespace(dl_ssm_bytes=bytes_, dl_ssm_prompt=prompt))
+    monkeypatch.setattr(torch, "empty", allocate)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: FakeStream(0))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: now[-1], raising=False)
+    return calls
+
+
+def prompt_on(stream, **kw):
+    cfg = dl.SsmConfig(2, 1, 64, 64, "f32")
+    q, v = torch.zeros(3, 64), torch.zeros(3, 128)
+    dl.dl_ssm_prompt(cfg, [0, 3], q, q, v, torch.zeros(3, 2), torch.zeros(2), None, None, None, None,
+                     torch.zeros(3, 128), stream=stream, **kw)
+
+
+@pytest.mark.parametrize("stream", [None, 11, 4096, FakeStream(4096), 0, FakeStream(0)])
+def test_workspace_comes_from_the_stream_of_the_call(fake_device, stream):
+    # memory that the allocator hands out on one stream may be in use there
+    # before the call, and is handed out again there after it
+    prompt_on(stream)
+    want = 11 if stream is None else getattr(stream, "cuda_stream", stream)
+    assert fake_device == [(want, want)]
+
+
+def test_workspace_of_the_special_stream_handles(fake_device):
+    # 1 is the legacy default stream by another name; what 2 means depends on the
+    # thread, so no memory can be tied to it
+    prompt_on(1)
+    assert fake_device == [(1, 0)]
+    with pytest.raises(ValueError, match="workspace"):
+        prompt_on(2)
+    prompt_on(2, workspace=torch.empty(512, dtype=torch.uint8))
+    assert fake_device[1:] == [(2, 11)]

@@ -78,3 +78,36 @@ def test_norm_codes_of_small_rows(peak, D):
                out, scales=sc)
     for row in range(3):
         check_codes(out[row].float().cpu(), sc[row].cpu(), w)
+
+
+# ------------------------------------------------------------------ scan
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["stream", "handle"])
+def test_prompt_on_a_given_stream_without_a_workspace(dtype, kind):
+    # the workspace of a call on a stream that is not the current one may not go
+    # to the current stream's next tensor while the call still uses it
+    t, T, H = {"bf16": T16, "f32": T32}[dtype], 4000, 2
+    cfg = dl.SsmConfig(H, 1, 128, 64, dtype)
+    z = dict(q=rnd(1, T, 128).to(t), k=rnd(2, T, 128).to(t), v=rnd(3, T, H * 64).to(t),
+             dt=0.1 * rnd(4, T, H).abs(), a=-rnd(5, H).abs())
+    z = {k: v.cuda() for k, v in z.items()}
+    nbytes = dl.dl_ssm_bytes(cfg, [0, T])
+    assert nbytes > 0
+
+    def call(**kw):
+        o, S1 = torch.empty(T, H * 64, dtype=t, device="cuda"), torch.empty(1, H, 64, 128, device="cuda")
+        torch.cuda.synchronize()
+        dl.dl_ssm_prompt(cfg, [0, T], z["q"], z["k"], z["v"], z["dt"], z["a"], None, None, None, S1, o, **kw)
+        return o, S1
+
+    want = call(workspace=torch.empty(nbytes, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        got = call(stream=side if kind == "stream" else side.cuda_stream)
+        after = [torch.empty(nbytes, dtype=torch.uint8, device="cuda").fill_(0x7f) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(bool((x == 0x7f).all()) for x in after)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert dl.dl_device_error(None) == (0, 0)
