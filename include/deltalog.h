@@ -228,9 +228,10 @@ int dl_state_destroy(dl_state* st);
  * their own: every buffer is the caller's, and the conventions above hold
  * (checks on the host first, asynchronous on `stream`, no device memory
  * allocated, tensors on the current device).  The prompt forms take packed
- * sequences: starts is a host array of n + 1 non-decreasing int32 >= 0, and
- * sequence s holds the rows starts[s] .. starts[s+1] - 1 (it may be empty);
- * rows outside [starts[0], starts[n]) are neither read nor written.  Lengths
+ * sequences: starts is a host array of n + 1 non-decreasing int32 from 0 to
+ * 2^31 - 1024 (beyond that DL_ERR_ARG, as for B of dl_conv_step), and sequence
+ * s holds the rows starts[s] .. starts[s+1] - 1 (it may be empty); rows outside
+ * [starts[0], starts[n]) are neither read nor written.  Lengths
  * travel by value with the launch, so a captured CUDA graph replays the
  * captured lengths; the single-token forms and dl_norm depend on nothing but
  * their buffers.  Row strides (ld*) count elements and may exceed the row, so

@@ -15,12 +15,17 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 bool dtype_ok(int t) { return t == DL_F32 || t == DL_BF16; }
 size_t elem(int t) { return t == DL_BF16 ? 2 : (t == DL_F32 ? 4 : 1); }
 
-// starts[0..n]: non-decreasing, >= 0.
+// Rows of a batch or tile behind the last one still have int32 numbers: the
+// largest step is a convolution's tile of 128 rows at most.
+constexpr int32_t kMaxRows = 0x7fffffff - 1023;
+
+// starts[0..n]: non-decreasing, 0 .. kMaxRows.
 int check_starts(int32_t n, const int32_t* starts) {
   if (n < 0 || starts == nullptr) return DL_ERR_ARG;
   if (starts[0] < 0) return DL_ERR_ARG;
   for (int32_t s = 0; s < n; ++s)
     if (starts[s + 1] < starts[s]) return DL_ERR_ARG;
+  if (starts[n] > kMaxRows) return DL_ERR_ARG;
   return DL_OK;
 }
 
@@ -151,7 +156,7 @@ int dl_conv_step(const dl_conv_config* cfg, int32_t B, const void* x, int64_t ld
                  const float* bias, void* h, void* y, int64_t ldy, void* stream) {
   const int rc = check_conv(cfg, B > 0, x, ldx, w, bias, h, h, y, ldy);
   if (rc != DL_OK) return rc;
-  if (B < 0 || (B > 0 && h == nullptr)) return DL_ERR_ARG;
+  if (B < 0 || B > kMaxRows || (B > 0 && h == nullptr)) return DL_ERR_ARG;
   if (B == 0) return DL_OK;
   const dl::ConvParams p = conv_params(*cfg, x, ldx, w, bias, h, h, y, ldy);
   return status(dl::launch_conv_step(p, B, cfg->W, cfg->in_dtype == DL_BF16, conv_wide(*cfg, p),

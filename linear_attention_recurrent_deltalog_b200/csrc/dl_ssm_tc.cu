@@ -422,7 +422,7 @@ dl_ssm_chunk_kernel(const TcParams p, const __grid_constant__ Table seqs, int se
     const int sl = seqs.find(w.tile);
     const int first = seqs.tile0[sl], ntiles = seqs.tile0[sl + 1] - first;
     w.begin = seqs.begin[sl] + (w.tile - first) * p.tile_tokens;
-    w.end = min(w.begin + p.tile_tokens, seqs.end[sl]);
+    w.end = w.begin + min(p.tile_tokens, seqs.end[sl] - w.begin);  // the sum stays an int32
     w.nch = (w.end - w.begin + kQ - 1) / kQ;
     w.cut = ntiles > 1;
     w.last = w.tile - first == ntiles - 1;

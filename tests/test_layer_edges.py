@@ -4,8 +4,10 @@ what they accept: no GPU is needed, fakes stand in for streams and the library."
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import types
 
+import numpy as np
 import pytest
 import torch
 
@@ -83,3 +85,32 @@ def test_workspace_of_the_special_stream_handles(fake_device):
         prompt_on(2)
     prompt_on(2, workspace=torch.empty(512, dtype=torch.uint8))
     assert fake_device[1:] == [(2, 11)]
+
+
+# ------------------------------------------------ rows up to the last int32s
+
+P = 1 << 20  # fake, aligned addresses: nothing here reaches a launch
+TOP = 2 ** 31 - 1024  # the last row number that a call may end at
+
+
+@pytest.mark.parametrize("start", [0, TOP - 3])
+@pytest.mark.parametrize("end", [TOP + 1, 2 ** 31 - 5, 2 ** 31 - 1])
+def test_row_numbers_near_the_end_of_int32_are_refused(start, end):
+    # the kernels form row numbers past the last one, of a batch or a tile
+    st = np.array([start, end], dtype=np.int32)
+    at, lib, n = st.ctypes.data, dl._lib, ctypes.c_size_t()
+    for dtype in ("bf16", "f32"):
+        conv, ssm = dl.ConvConfig(64, 4, dtype), dl.SsmConfig(2, 1, 64, 64, dtype)
+        x = dl.dl_ssm_io(q=P, k=P, v=P, dt=P, a=P, o=2 * P, ldq=64, ldk=64, ldv=128, lddt=2, ldo=128)
+        assert lib.dl_conv_prompt(conv.ref, 1, at, P, 64, P, None, None, None, 2 * P, 64, None) == dl.DL_ERR_ARG
+        assert lib.dl_ssm_bytes(ssm.ref, 1, at, ctypes.byref(n)) == dl.DL_ERR_ARG
+        assert lib.dl_ssm_prompt(ssm.ref, 1, at, ctypes.byref(x), None, None, P, 1 << 50, None) == dl.DL_ERR_ARG
+        assert lib.dl_conv_step(conv.ref, end, P, 64, P, None, P, 2 * P, 64, None) == dl.DL_ERR_ARG
+
+
+def test_row_numbers_up_to_the_limit_are_planned():
+    st = np.array([TOP - 300, TOP], dtype=np.int32)
+    n = ctypes.c_size_t()
+    ssm = dl.SsmConfig(2, 1, 64, 64)
+    assert dl._lib.dl_ssm_bytes(ssm.ref, 1, st.ctypes.data, ctypes.byref(n)) == dl.DL_OK
+    assert n.value == dl.dl_ssm_bytes(ssm, [0, 300])

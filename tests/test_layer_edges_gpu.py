@@ -3,10 +3,12 @@ number formats and of their launch forms, against 64-bit definitions."""
 
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 from linear_attention_recurrent_deltalog_b200 import deltalog as dl
+from tests import layer_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +113,25 @@ def test_prompt_on_a_given_stream_without_a_workspace(dtype, kind):
         assert all(bool((x == 0x7f).all()) for x in after)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert dl.dl_device_error(None) == (0, 0)
+
+
+# ------------------------------------------------------------------ convolution
+
+@pytest.mark.parametrize("C", [1, 4])  # element by element, four channels at a time
+def test_conv_of_the_last_row_numbers(C):
+    # offsets past 32 bits, and row numbers up to the last one allowed
+    top, W, lens = 2 ** 31 - 1024, 4, [300, 0, 37]
+    st = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64) + top - sum(lens)
+    x = torch.empty(top, C, dtype=T16, device="cuda")
+    y = torch.empty(top, C, dtype=T16, device="cuda")
+    rows = rnd(1, sum(lens), C).to(T16)
+    x[-sum(lens):] = rows.cuda()
+    y[-500:] = 7.0
+    w, h = rnd(2, C, W), rnd(3, 3, W - 1, C).to(T16)
+    h1 = torch.empty(3, W - 1, C, dtype=T16, device="cuda")
+    dl.dl_conv_prompt(dl.ConvConfig(C, W, "bf16", silu=False), st, x, w.cuda(), None, h.cuda(), h1, y)
+    want, mag, hw = ref.conv(rows, st - st[0], w, None, h, False)
+    got = y[-sum(lens):].double().cpu()
+    assert ((got - want).abs() <= ref.conv_tol(mag, W, T16)).all()
+    assert torch.equal(h1.double().cpu(), hw)
+    assert (y[-500:-sum(lens)] == 7).all()
