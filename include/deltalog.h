@@ -243,7 +243,10 @@ int dl_state_destroy(dl_state* st);
 enum dl_out_dtype { DL_E4M3 = 2 /* 8 bits: 4 exponent, 3 mantissa, largest value 448 (e4m3) */ };
 
 /* dl_conv_config.flags */
-enum dl_conv_flags { DL_CONV_SILU = 1 /* y * sigmoid(y) on the way out */ };
+enum dl_conv_flags {
+  DL_CONV_SILU = 1 /* y * sigmoid(y) on the way out: fp32 rows to 8 * 2^-24 of its value where
+                      that is normal, bf16 rows rounded once (-0 where it is below 2^-119) */
+};
 
 /* Depthwise causal convolution of width W in {2, 3, 4} over C channels. */
 typedef struct dl_conv_config {

@@ -135,3 +135,24 @@ def test_conv_of_the_last_row_numbers(C):
     assert ((got - want).abs() <= ref.conv_tol(mag, W, T16)).all()
     assert torch.equal(h1.double().cpu(), hw)
     assert (y[-500:-sum(lens)] == 7).all()
+
+
+def test_conv_silu_of_fp32_rows_over_its_range():
+    # one tap of 1: the sum is x itself, so y is the activation alone.  Its
+    # roundings, in units of 2^-24 of the value: the exponential 4 (2 ulp), which
+    # counts half to whole, and one each for 1 + e, the quotient and the product:
+    # 8 in all.  Below -87.3 e^x has no normal fp32: half a step of 2^-149, times |x|.
+    x = torch.cat([torch.linspace(-106, 106, 40001), torch.linspace(-89, -87, 4001),
+                   torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3e38, -3e38, 1e-45])]).to(T32)
+    for C in (1, 4):
+        n = x.numel() // C * C
+        xg = x[:n].view(-1, C).cuda()
+        w = torch.zeros(C, 2, device="cuda")
+        w[:, 1] = 1.0
+        y = torch.empty_like(xg)
+        dl.dl_conv_prompt(dl.ConvConfig(C, 2, "f32"), [0, n // C], xg, w, None, None, None, y)
+        xd = x[:n].double()
+        want = xd / (1 + torch.exp(-xd))
+        tol = want.abs() * 8 * U + (xd.abs() + 1) * 4 * 2.0 ** -149
+        bad = (y.double().cpu().view(-1) - want).abs() > tol
+        assert not bad.any(), (x[:n][bad][:5], y.cpu().view(-1)[bad][:5], int(bad.sum()))
