@@ -390,8 +390,13 @@ def _on_device(names: str, *tensors) -> Optional[int]:
 
 
 def _stream_on(dev: int, stream) -> int:
-    """The given stream's handle, or the current one's of the current device ``dev``."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    """The given stream's handle, or the current one's of the current device ``dev``, to which a
+    given one has to belong (a bare handle does not say)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream: must belong to the current CUDA device {dev}, not {stream}")
+    return _stream(stream)
 
 
 def _workspace(nbytes: int, device, stream) -> torch.Tensor:
@@ -562,6 +567,7 @@ def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o,
     the call, on its stream, when None)."""
     at, n, rows, keep = _starts(starts)
     io, p0, p1, dev = _ssm_io(cfg, rows, n, q, k, v, dt, a, d, dt_bias, o, S0, S1)
+    on = _stream_on(dev, stream)
     if workspace is None:
         workspace = _workspace(dl_ssm_bytes(cfg, keep), q.device, stream)
     elif not isinstance(workspace, torch.Tensor):
@@ -571,7 +577,7 @@ def dl_ssm_prompt(cfg: SsmConfig, starts, q, k, v, dt, a, d, dt_bias, S0, S1, o,
         raise ValueError("workspace: must be contiguous")
     _on_device("workspace", workspace)
     rc = _lib.dl_ssm_prompt(cfg.ref, n, at, io, p0, p1,
-                            workspace.data_ptr() if nb else None, nb, _stream_on(dev, stream))
+                            workspace.data_ptr() if nb else None, nb, on)
     if rc:
         _check(rc, "dl_ssm_prompt")
 

@@ -114,3 +114,17 @@ def test_row_numbers_up_to_the_limit_are_planned():
     ssm = dl.SsmConfig(2, 1, 64, 64)
     assert dl._lib.dl_ssm_bytes(ssm.ref, 1, st.ctypes.data, ctypes.byref(n)) == dl.DL_OK
     assert n.value == dl.dl_ssm_bytes(ssm, [0, 300])
+
+
+# ------------------------------------------------- streams of another device
+
+def test_stream_of_another_device_is_refused(fake_device):
+    other = FakeStream(4096)
+    other.device_index = 1
+    for kw in ({}, {"workspace": torch.empty(512, dtype=torch.uint8)}):
+        with pytest.raises(ValueError, match="stream: .*current CUDA device"):
+            prompt_on(other, **kw)
+    assert fake_device == []
+    bare = types.SimpleNamespace(cuda_stream=4096)  # another library's: a handle and no more
+    prompt_on(bare)
+    assert fake_device == [(4096, 4096)]
