@@ -285,12 +285,20 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+def _cuda_calls():
+    """-> (current device's index, handle of a device's current stream), by torch's quick forms where
+    it has them: current_stream() builds a Stream object per call."""
+    return (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+            getattr(torch._C, "_cuda_getCurrentRawStream",
+                    lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+
+
+_current_device, _current_stream = _cuda_calls()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        if torch.cuda.is_initialized():
-            # the handle alone: current_stream() would build a Stream object per call
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return None
+        return _current_stream(_current_device()) if torch.cuda.is_initialized() else None
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -381,7 +389,7 @@ def _rows(t, name: str, rows: int, cols: int, dtype: torch.dtype) -> int:
 
 def _on_device(names: str, *tensors) -> Optional[int]:
     """Every tensor (or None) on the current CUDA device, whose stream the call uses."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
+    dev = _current_device() if torch.cuda.is_initialized() else None
     for t in tensors:
         if t is not None and t.get_device() != dev:
             name = names.split()[[x is t for x in tensors].index(True)]
@@ -393,7 +401,7 @@ def _stream_on(dev: int, stream) -> int:
     """The given stream's handle, or the current one's of the current device ``dev``, to which a
     given one has to belong (a bare handle does not say)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_stream(dev)
     if getattr(stream, "device_index", dev) != dev:
         raise ValueError(f"stream: must belong to the current CUDA device {dev}, not {stream}")
     return _stream(stream)

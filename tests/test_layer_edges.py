@@ -56,7 +56,7 @@ def fake_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(handle))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: FakeStream(0))
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: now[-1], raising=False)
+    monkeypatch.setattr(dl, "_current_stream", lambda dev: now[-1])
     return calls
 
 
@@ -128,3 +128,21 @@ def test_stream_of_another_device_is_refused(fake_device):
     bare = types.SimpleNamespace(cuda_stream=4096)  # another library's: a handle and no more
     prompt_on(bare)
     assert fake_device == [(4096, 4096)]
+
+
+# --------------------------------------------------- a torch without shortcuts
+
+def test_current_device_and_stream_by_torchs_public_calls(monkeypatch):
+    # the quick forms are private names of torch: without them the public ones serve
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: FakeStream(100 + dev))
+    device, stream = dl._cuda_calls()
+    assert device() == 3 and stream(3) == 103
+    monkeypatch.setattr(dl, "_current_device", device)
+    monkeypatch.setattr(dl, "_current_stream", stream)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    assert dl._stream(None) == 103 and dl._stream_on(2, None) == 102
+    with pytest.raises(ValueError, match="x: .*current CUDA device"):
+        dl._on_device("x", torch.zeros(1))
