@@ -12,6 +12,7 @@ from __future__ import annotations
 import argparse
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -33,6 +34,30 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+SCAN = "dl_ssm_tc.cu"
+
+
+def start_registers() -> int:
+    """Registers a thread of the scan's chunk kernel has to start with."""
+    with open(os.path.join(CSRC, SCAN)) as f:
+        return int(re.search(r"kStartRegs = (\d+)", f.read()).group(1))
+
+
+def check_registers(ptxas: str) -> None:
+    """Raises where the compiler gave a chunk kernel fewer registers than its roles share out (the
+    launch refuses such a kernel, since its warps would wait for registers for good)."""
+    need, name, seen = start_registers(), "", 0
+    for line in ptxas.splitlines():
+        if m := re.search(r"Compiling entry function '(\S+)'", line):
+            name = m.group(1)
+        elif "dl_ssm_chunk_kernel" in name and (m := re.search(r"Used (\d+) registers", line)):
+            seen += 1
+            if int(m.group(1)) < need:
+                raise RuntimeError(f"{name}: {m.group(1)} registers a thread, its roles share out {need}")
+    if seen == 0:
+        raise RuntimeError(f"{SCAN}: no chunk kernel's registers in the compiler's output")
 
 
 def _deps() -> list:
@@ -59,7 +84,7 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
     for src in sources:
         obj = os.path.join(BUILD, os.path.basename(src).replace(".cu", ".o"))
         cmd = [cc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
-        if ptxas_info:
+        if ptxas_info or os.path.basename(src) == SCAN:
             cmd += ["-Xptxas", "-v"]
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -73,8 +98,11 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
             sys.stdout.write(out)
         if p.returncode != 0:
             failed.append(src)
+        if os.path.basename(src) == SCAN:
+            scan_out = out
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(os.path.basename(f) for f in failed))
+    check_registers(scan_out)
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-lrt", "-ldl", "-lpthread"]
     if verbose:

@@ -11,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+from linear_attention_recurrent_deltalog_b200 import build
 from linear_attention_recurrent_deltalog_b200 import deltalog as dl
 
 
@@ -146,3 +147,24 @@ def test_current_device_and_stream_by_torchs_public_calls(monkeypatch):
     assert dl._stream(None) == 103 and dl._stream_on(2, None) == 102
     with pytest.raises(ValueError, match="x: .*current CUDA device"):
         dl._on_device("x", torch.zeros(1))
+
+
+# ------------------------------------- registers that the scan's roles share out
+
+PTXAS = """ptxas info    : Compiling entry function '_ZN2dl19dl_ssm_chunk_kernelILi128EEEv' for 'sm_100a'
+ptxas info    : Function properties for _ZN2dl19dl_ssm_chunk_kernelILi128EEEv
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used {} registers, used 1 barriers
+ptxas info    : Compiling entry function '_ZN2dl18dl_ssm_join_kernelEv' for 'sm_100a'
+ptxas info    : Used 32 registers, used 0 barriers
+"""
+
+
+def test_build_refuses_a_scan_kernel_with_too_few_registers():
+    # the launch would refuse it: its warps' shares add up against what a block starts with
+    need = build.start_registers()
+    assert need >= 24 and need % 8 == 0
+    build.check_registers(PTXAS.format(need))
+    for text in (PTXAS.format(need - 8), PTXAS.format(need).replace("chunk", "other")):
+        with pytest.raises(RuntimeError, match="registers"):
+            build.check_registers(text)
