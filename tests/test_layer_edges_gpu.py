@@ -82,6 +82,34 @@ def test_norm_codes_of_small_rows(peak, D):
         check_codes(out[row].float().cpu(), sc[row].cpu(), w)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("rows,D", [(3, 1), (5, 129), (9, 1000), (4, 4096), (2, 6152), (2, 16384), (3, 9001),
+                                    (9000, 520)])
+def test_norm_scales_and_codes_tightly(rows, D, block, dtype):
+    # In units of 2^-24 of the value: x + res is rounded once, whatever cancels.
+    # The mean of squares: 2 of each square, D of the sum of positive terms, 1 each
+    # of the division and of eps, halved by the root; root, reciprocal, two products
+    # and the sum's own 1: D / 2 + 7 for n, one more for the scale.  The mean's part
+    # is the whole row's and leaves n / amax as it is: 3 of n, 3 of amax, the
+    # quotient and the product make 8 before the code's rounding, half a step of
+    # e4m3 (2^-4 of it, at least half of 2^-9).
+    t = {"bf16": T16, "f32": T32}[dtype]
+    x, r, w = rnd(1, rows, D).to(t), rnd(2, rows, D).to(t), 1 + 0.2 * rnd(3, D)
+    step = block or D
+    out = torch.empty(rows, D, dtype=T8, device="cuda")
+    sc = torch.empty(rows, -(-D // step), device="cuda")
+    dl.dl_norm(dl.NormConfig(D, dtype, "e4m3", block=block, eps=1e-5), x.cuda(), w.cuda(), out, res=r.cuda(),
+               scales=sc)
+    _, n = ref.norm(x, r, w, 1e-5)
+    amax = torch.stack([p.abs().max(1).values for p in n.split(step, 1)], 1)
+    assert ((sc.double().cpu() - amax / 448).abs() <= amax / 448 * ((0.5 * D + 8.1) * U)).all()
+    want = n * (448 / amax).repeat_interleave(step, 1)[:, :D]
+    pre = want.abs() * (8.1 * U)
+    err = (out.double().cpu() - want).abs()
+    assert (err <= torch.clamp((want.abs() + pre) * 2.0 ** -4, min=2.0 ** -10) + pre).all()
+
+
 # ------------------------------------------------------------------ scan
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -156,3 +184,22 @@ def test_conv_silu_of_fp32_rows_over_its_range():
         tol = want.abs() * 8 * U + (xd.abs() + 1) * 4 * 2.0 ** -149
         bad = (y.double().cpu().view(-1) - want).abs() > tol
         assert not bad.any(), (x[:n][bad][:5], y.cpu().view(-1)[bad][:5], int(bad.sum()))
+
+
+@pytest.mark.parametrize("dtype,B,C,W", [("bf16", 509, 4352, 4), ("bf16", 67, 8191, 4), ("bf16", 1030, 1024, 3),
+                                         ("bf16", 250, 8191, 2), ("f32", 301, 4352, 4), ("f32", 131, 4353, 2)])
+def test_conv_step_of_several_sequences_a_thread(dtype, B, C, W):
+    # more than the 113,664 threads of a wave at four channels (or one) each: a
+    # thread takes 2 to 8 sequences, four at a time, with a rest in the last batch
+    # and a shorter share in the last thread
+    t = {"bf16": T16, "f32": T32}[dtype]
+    x, w, b, h = rnd(1, B, C).to(t), rnd(2, C, W), rnd(3, C), rnd(4, B, W - 1, C).to(t)
+    hg, y = h.cuda(), torch.full((B + 1, C), 7.0, dtype=t, device="cuda")
+    dl.dl_conv_step(dl.ConvConfig(C, W, dtype), x.cuda(), w.cuda(), b.cuda(), hg, y[:B])
+    rows = torch.cat([h, x[:, None]], 1).double()
+    s = b.double() + (rows * w.double().t()).sum(1)
+    mag = b.double().abs() + (rows * w.double().t()).abs().sum(1)
+    want = ref.silu(s)
+    tol = ref.conv_tol(1.1 * mag + want.abs(), W, t)
+    assert ((y[:B].double().cpu() - want).abs() <= tol).all()
+    assert torch.equal(hg.double().cpu(), rows[:, 1:]) and (y[B] == 7).all()
