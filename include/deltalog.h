@@ -318,7 +318,13 @@ int dl_ssm_bytes(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, siz
  * prompt taken in pieces).  The state of a sequence can be loaded by
  * dl_state_load_seqs or stepped by dl_ssm_step.  workspace: 256-byte aligned,
  * of workspace_bytes >= dl_ssm_bytes (NULL when that is 0), written by the
- * call: calls that may run at the same time need one each. */
+ * call: calls that may run at the same time need one each.
+ * Decays, weights and states are fp32, and S1 is right to fp32's rounding for
+ * both row types.  fp32 rows: o too, its sums in the order of the tokens.  bf16
+ * rows: what o sums, in fp32, are products of values rounded to bf16 first (each
+ * token's weight q.k dt e^{..}, or the state that q reads, once per term: 2^-8 of
+ * it at most), before o's own rounding: 0.0022 of o's norm in all, of which o's
+ * rounding alone makes 0.0017.  dl_ssm_step rounds o only. */
 int dl_ssm_prompt(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, const dl_ssm_io* io,
                   const float* S0, float* S1, void* workspace, size_t workspace_bytes,
                   void* stream);
@@ -328,7 +334,8 @@ int dl_ssm_prompt(const dl_ssm_config* cfg, int32_t n, const int32_t* starts, co
 int dl_ssm_step(const dl_ssm_config* cfg, int32_t B, const dl_ssm_io* io, float* S, void* stream);
 
 /* Root-mean-square norm of rows, after the addition of a residual:
- *   h = x + res,  n = h / sqrt(mean(h^2) + eps) * w,  all in fp32.
+ *   h = x + res,  n = h / sqrt(mean(h^2) + eps) * w,  all in fp32 (a sum of
+ *   squares beyond its range makes n = 0).
  * out_dtype DL_F32 / DL_BF16: out = n, rounded once.  DL_E4M3: per block of
  * `block` channels (0: the whole row) scale = amax / 448 and code =
  * e4m3(n * (448 / amax)), round to nearest even; a block with amax < 2^-120
