@@ -2,17 +2,18 @@
 //     y[t, c] = act(bias[c] + sum_j w[c, j] x[t - W + 1 + j, c]),
 // for packed prompts and for single tokens.  Rows before a sequence's first
 // token come from its state (its last W - 1 input rows, oldest first).  Two
-// flops a byte: bound by memory (T = 8192, C = 4352, W = 4, bf16: 32 us, 4.5 TB/s
-// of rows in and out; fewer instructions or reciprocals, or rows further ahead,
-// made it no faster, which leaves the 8-byte accesses: fp32 rows of the same
-// bytes take 29).  A thread owns VEC neighbouring channels: four
-// where the rows allow 8-byte (bf16) or 16-byte (fp32) accesses, else one.
+// flops a byte: bound by memory (T = 8192, C = 4352, W = 4, bf16: 31 us in a
+// replayed graph, 4.7 TB/s of rows in and out; fewer instructions or reciprocals, or
+// rows further ahead, made it no faster, and the 8-byte accesses alone do not hold
+// it: fp32 rows of the same bytes, 16 at a time, take as long, both 29 without the
+// activation).  A thread owns VEC neighbouring channels: four where the rows allow
+// 8-byte (bf16) or 16-byte (fp32) accesses, else one.
 // Eight bf16 channels a thread were slower: their taps (fp32, 128 bytes a
 // thread at W = 4) and the rows in flight leave room for a third of the warps.
 // A prompt's thread walks down the tokens of its tile with the last W - 1 rows
 // in registers, so an input row is read once, but for the W - 1 rows at the
 // head of a tile; a step's thread takes several sequences, so that the taps
-// are read once for all of them (B = 512, C = 4352: 6.6 us, 41 with eight channels
+// are read once for all of them (B = 512, C = 4352: 5.4 us, 41 with eight channels
 // and one sequence a thread).
 #include "dl_layer.cuh"
 

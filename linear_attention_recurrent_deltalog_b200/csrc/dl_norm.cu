@@ -274,7 +274,20 @@ cudaError_t norm_t(const NormParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The team and the 8-channel pieces a thread holds, by the row's length.
+// The team and the 8-channel pieces a thread holds, by the row's length: the
+// smallest team that holds a row in two pieces a thread (one below 257, where a
+// warp or half of one is enough, and between 513 and 1024), since lanes without
+// channels cost as much as others and the root is a team's work.  bf16 rows with the
+// residual to e4m3, 2^23 channels in all, in us for this team and the others that
+// hold the row (threads x pieces):
+//     128    16x1 11.7   32x1 20.3   32x2 28.4
+//     256    32x1 11.4   32x2 15.5   64x1 19.5   128x1 33.0
+//     512    32x2 10.2   64x1 11.7   128x1 18.7
+//     1024   128x1 11.3  64x2 10.6   128x2 15.6  32x4 18.8
+//     2048   128x2 10.5  256x1 11.7  256x2 15.8
+//     4096   256x2 10.9  512x1 15.3  512x2 18.5
+//     8192   512x2 12.5  512x4 17.7
+// The other types order alike (fp32 rows of 767: 32x4 42, 128x1 20, 64x2 19).
 template <typename T, typename TO, bool VEC>
 cudaError_t norm_by_length(const NormParams& p, cudaStream_t s) {
   if (p.D <= 128) return norm_t<T, TO, 16, 1, VEC>(p, s);

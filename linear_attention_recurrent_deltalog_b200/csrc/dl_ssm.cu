@@ -43,7 +43,8 @@ __device__ __forceinline__ float rows_step(float4 (&s)[WarpRows<DK>::NV], float4
 // -------------------------------------------------------------- one token
 //
 // Bound by HBM: the state is read and written once (B = 256, H = 64, d = 128 x 64:
-// 160 us, 6.7 TB/s, a copy's rate).  One CTA per head; a warp
+// 160 us, 6.75 TB/s: a torch copy of 2 GB runs at 6.55, the fastest stream measured
+// at 6.83).  One CTA per head; a warp
 // owns 16 rows of the state in registers (WarpRows' geometry: a lane holds four
 // neighbouring key channels of each of its rows) and issues all its loads before
 // it needs one, and the 16 row sums S q finish in one butterfly.
@@ -319,7 +320,16 @@ cudaError_t launch_ssm_step(const SsmParams& p, int B, int dk, int dv, bool bf16
 // Tile length: with two CTAs an SM most of the latency is hidden, so a call
 // takes about its tokens spread over as many, or its longest sequence.  Where the
 // latter is three times the former or more, sequences are cut to the former's
-// length (the cut reads k and v twice and costs two launches).
+// length (the cut reads k and v twice and costs two launches).  Both sides, in us
+// (median of replayed graphs; ratio: the longest to the spread):
+//     ratio 4.6, T = 2048 H = 16 d = 128 x 64     209 whole, 147 in 3, 124 in 4 (taken)
+//     ratio 4.6, T = 300 H = 16 d = 64 x 64       26 whole, 20.5 in 4 (taken)
+//     ratio 2.8, T = 517 (3) H = 16 d = 64 x 64   29 whole (taken), 29 in 2
+//     ratio 2.4, T = 2048 (8) H = 8 d = 128 x 64  72 whole (taken), 93 in 2
+//     ratio 2.3, T = 2048 H = 32 d = 128 x 64     211 whole (taken), 215 in 2
+// Finer cuts than the spread gain in those (25 us in 6, 65 in 6, 182 in 8), less
+// surely below (ratio 1.2: 283 whole and 324 in 4 at H = 64 d = 128 x 64, 201 and 190
+// at H = 32 d = 64 x 128).
 SsmPlan plan_ssm_scan(int H, int dk, int dv, int n, const int32_t* starts, int sms) {
   constexpr long long kMinTile = 64;
   long long longest = 0;

@@ -27,10 +27,11 @@
 // dl_ssm_join_kernel turns those into the state each tile enters with, and the
 // main launch starts from them.
 //
-// T = 8192, H = 64, d = 128 x 64, one sequence in four tiles: 114 us, of which the
-// states take 38 (2.4 a chunk), the join 6 and the main launch 76 (4.8 a chunk,
-// 1.7 of them its MMAs').  What bounds a chunk is the element work: 4,000 of a
-// scheduler's 7,500 cycles issue an instruction, the tensor pipe is busy for 0.45
+// T = 8192, H = 64, d = 128 x 64, one sequence in four tiles: 114 us a pass in a row
+// of passes.  Each launch alone, caches cold, under the profiler: 38 us for the
+// states (2.4 a chunk), 7 for the join, 75 for the main launch (4.7 a chunk, 1.8 of
+// them its MMAs').  What bounds a chunk is the element work: 4,490 of a
+// scheduler's 8,100 cycles issue an instruction, the tensor pipe is busy for 0.38
 // of them.  M and w o V are TMEM operands because shared memory is next: an MMA
 // with both operands there reads 128 bytes a cycle, all it can deliver, and w o V
 // there, written once and read with K three times over, cost 0.3 MB more a chunk.
@@ -1159,8 +1160,15 @@ int cta_pairs(int H, int G, int dv) {
 }  // namespace
 
 // Tile length: one CTA runs per SM, and a cut tile costs a second walk over
-// its k and v (kStatesCost of a full one: 2.4 of 4.8 us a chunk), so take the length whose
-// waves of CTAs finish first.
+// its k and v (kStatesCost of a full one: 2.4 of 4.7 us a chunk), so take the length whose
+// waves of CTAs finish first.  One sequence, in us by parts (* taken), each point
+// the median of replayed graphs:
+//     T = 8192, H = 64, d = 128 x 64   243 whole, 138 in 3, 110 in 4*, 143 in 5, 114 in 10
+//     T = 8192, H = 64, d = 64 x 64    231 whole, 131 in 3, 102 in 4*, 129 in 5, 102 in 10
+//     T = 2048, H = 16, d = 64 x 64    62 whole, 34 in 4, 25 in 8 and more*
+// At d_k = 64 D is half as wide and the same lengths win.  T = 6001 in 24 sequences
+// stays whole (81, 117 in halves).  Three uneven sequences of 8192 tokens are where
+// the estimate errs: 142 in 4 parts*, 122 in 5.
 SsmPlan plan_ssm(int H, int G, int dk, int dv, int n, const int32_t* starts, int sms) {
   constexpr double kStatesCost = 0.5, kTileCost = 1.0;  // in chunks
   const int pairs = cta_pairs(H, G, dv);
