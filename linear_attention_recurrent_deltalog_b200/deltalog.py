@@ -410,7 +410,7 @@ def _stream_on(dev: int, stream) -> int:
 def _workspace(nbytes: int, device, stream) -> torch.Tensor:
     """Memory for one call on ``stream``, from that stream's pool: what it held before and what it
     is given to afterwards then run before and after the call."""
-    if stream is None:
+    if stream is None or nbytes == 0:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = _stream(stream)

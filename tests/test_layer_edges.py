@@ -88,6 +88,18 @@ def test_workspace_of_the_special_stream_handles(fake_device):
     assert fake_device[1:] == [(2, 11)]
 
 
+def test_call_without_a_workspace_takes_any_stream_handle(fake_device):
+    def none(cfg, n, at, out):
+        out._obj.value = 0
+        return 0
+
+    called = []
+    dl._lib.dl_ssm_bytes = none
+    dl._lib.dl_ssm_prompt = lambda *a: called.append((a[6], a[7], a[8])) or 0
+    prompt_on(2)
+    assert called == [(None, 0, 2)]
+
+
 # ------------------------------------------------ rows up to the last int32s
 
 P = 1 << 20  # fake, aligned addresses: nothing here reaches a launch
